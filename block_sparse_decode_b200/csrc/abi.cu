@@ -557,6 +557,167 @@ qsa_status qsa_sparse_prefill(const qsa_dims *dims, const qsa_cache *cache, int3
   return st;
 }
 
+qsa_status qsa_qk_norm_rope(int32_t N, int32_t Hq, int32_t Hk, int32_t D, const int32_t *pos,
+                            const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                            const float *q_weight, const float *k_weight, float eps,
+                            const float *rope, int32_t max_pos, int32_t rot_dim,
+                            int32_t interleaved, void *q_out, void *k_out, qsa_stream_t stream) {
+  QSA_RANGE("qsa_qk_norm_rope");
+  try {
+    if (N < 0) return fail(QSA_ERR_INVALID_ARG, "N < 0");
+    if (Hq <= 0 || Hk < 0 || Hq > 65536 || Hk > 65536)
+      return fail(QSA_ERR_INVALID_ARG, "Hq=%d / Hk=%d heads out of range", Hq, Hk);
+    if (D != 64 && D != 128)
+      return fail(QSA_ERR_UNSUPPORTED, "head dim D=%d unsupported (64, 128)", D);
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0)
+      return fail(QSA_ERR_UNSUPPORTED, "rot_dim=%d must be a multiple of 16 in [0, D]", rot_dim);
+    if (!(eps >= 0.f)) return fail(QSA_ERR_INVALID_ARG, "eps must be >= 0");
+    if (rot_dim > 0 && max_pos <= 0) return fail(QSA_ERR_INVALID_ARG, "max_pos must be positive");
+    if (N == 0) return ok();
+    if (pos == nullptr || q == nullptr || q_out == nullptr ||
+        (Hk > 0 && (k == nullptr || k_out == nullptr)) || (rot_dim > 0 && rope == nullptr))
+      return fail(QSA_ERR_INVALID_ARG, "an argument array is NULL");
+    if (q_stride < (int64_t)Hq * D || (Hk > 0 && k_stride < (int64_t)Hk * D) ||
+        q_stride % 8 != 0 || (Hk > 0 && k_stride % 8 != 0))
+      return fail(QSA_ERR_INVALID_ARG,
+                  "token strides must hold the heads and be multiples of 8 elements");
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(q_weight) || !aligned16(k_weight) ||
+        !aligned16(rope) || (Hk > 0 && (!aligned16(k) || !aligned16(k_out))))
+      return fail(QSA_ERR_INVALID_ARG, "an array is not 16-byte aligned");
+    if ((q == q_out && q_stride != (int64_t)Hq * D) ||
+        (Hk > 0 && k == k_out && k_stride != (int64_t)Hk * D))
+      return fail(QSA_ERR_INVALID_ARG, "in place needs dense rows");
+    QSA_ERRWORD(err);
+    return cuda_status(launch_norm_rope(N, Hq, Hk, D, pos, q, q_stride, k, k_stride, q_weight,
+                                        k_weight, eps, rope, max_pos, rot_dim, interleaved, q_out,
+                                        k_out, err, reinterpret_cast<cudaStream_t>(stream)),
+                       "qsa_qk_norm_rope launch");
+  } catch (...) {
+    return fail(QSA_ERR_CUDA, "qsa_qk_norm_rope: internal exception");
+  }
+}
+
+namespace {
+
+// Checks shared by the calls over the rows of appended chunks.
+qsa_status check_chunks(const qsa_dims *dims, const qsa_cache *cache, int32_t S, int32_t Nq) {
+  QSA_TRY(check_dims(dims));
+  QSA_TRY(check_cache(cache, true, false));
+  if (S < 0 || S > 65535 || S > cache->num_seqs)
+    return fail(QSA_ERR_INVALID_ARG, "S=%d outside [0, 65535] or over the block_table rows %d", S,
+                cache->num_seqs);
+  if (Nq < 0 || Nq > 65535) return fail(QSA_ERR_INVALID_ARG, "Nq=%d outside [0, 65535]", Nq);
+  return QSA_OK;
+}
+
+}  // namespace
+
+size_t qsa_chunk_attention_workspace_size(const qsa_dims *dims, int32_t S, int32_t Nq) {
+  if (dims == nullptr || S <= 0 || Nq <= 0 || dims->Hkv <= 0 || dims->Hq <= 0) return 0;
+  return chunk_attention_ws_bytes(*dims, S, Nq);
+}
+
+qsa_status qsa_chunk_attention(const qsa_dims *dims, const qsa_cache *cache, int32_t S,
+                               const int32_t *seq_lens, const int32_t *row_start, int32_t Nq,
+                               const void *q, void *out, int32_t out_is_bf16, float *lse_out,
+                               void *ws, size_t ws_bytes, qsa_stream_t stream) {
+  QSA_RANGE("qsa_chunk_attention");
+  try {
+    QSA_TRY(check_chunks(dims, cache, S, Nq));
+    if (S == 0 || Nq == 0) return ok();
+    if (seq_lens == nullptr || row_start == nullptr || q == nullptr || out == nullptr)
+      return fail(QSA_ERR_INVALID_ARG, "an argument array is NULL");
+    if (!aligned16(q) || !aligned16(out) || !aligned16(ws))
+      return fail(QSA_ERR_INVALID_ARG, "q / out / ws not 16-byte aligned");
+    const size_t need = chunk_attention_ws_bytes(*dims, S, Nq);
+    if (need > 0 && (ws == nullptr || ws_bytes < need))
+      return fail(QSA_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    QSA_ERRWORD(err);
+    return cuda_status(launch_chunk_attention(*dims, *cache, S, seq_lens, row_start, Nq, q, out,
+                                              out_is_bf16, lse_out, ws, err,
+                                              reinterpret_cast<cudaStream_t>(stream)),
+                       "qsa_chunk_attention launch");
+  } catch (...) {
+    return fail(QSA_ERR_CUDA, "qsa_chunk_attention: internal exception");
+  }
+}
+
+size_t qsa_attention_mass_workspace_size(const qsa_dims *dims, int32_t S, int32_t Nq) {
+  if (dims == nullptr || S <= 0 || Nq <= 0 || dims->Hkv <= 0 || dims->Hq <= 0) return 0;
+  return attention_mass_ws_bytes(*dims, S, Nq);
+}
+
+qsa_status qsa_attention_mass(const qsa_dims *dims, const qsa_cache *cache, int32_t S,
+                              const int32_t *seq_lens, const int32_t *row_start, int32_t Nq,
+                              const void *q, const float *lse, const float *mass_in, float *mass,
+                              int32_t ld_mass, void *ws, size_t ws_bytes, qsa_stream_t stream) {
+  QSA_RANGE("qsa_attention_mass");
+  try {
+    QSA_TRY(check_chunks(dims, cache, S, Nq));
+    if (ld_mass <= 0) return fail(QSA_ERR_INVALID_ARG, "ld_mass must be positive");
+    if (S == 0) return ok();
+    if (seq_lens == nullptr || row_start == nullptr || mass == nullptr ||
+        (Nq > 0 && (q == nullptr || lse == nullptr)))
+      return fail(QSA_ERR_INVALID_ARG, "an argument array is NULL");
+    if (!aligned16(q) || !aligned16(ws))
+      return fail(QSA_ERR_INVALID_ARG, "q / ws not 16-byte aligned");
+    const size_t need = attention_mass_ws_bytes(*dims, S, Nq);
+    if (need > 0 && (ws == nullptr || ws_bytes < need))
+      return fail(QSA_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    QSA_ERRWORD(err);
+    return cuda_status(launch_attention_mass(*dims, *cache, S, seq_lens, row_start, Nq, q, lse,
+                                             mass_in, mass, ld_mass, ws, err,
+                                             reinterpret_cast<cudaStream_t>(stream)),
+                       "qsa_attention_mass launch");
+  } catch (...) {
+    return fail(QSA_ERR_CUDA, "qsa_attention_mass: internal exception");
+  }
+}
+
+size_t qsa_evict_workspace_size(int32_t B, int32_t ld_mass, int32_t keep) {
+  (void)B;
+  (void)ld_mass;
+  (void)keep;
+  return 0;
+}
+
+qsa_status qsa_evict(const qsa_dims *dims, const qsa_cache *cache, int32_t B,
+                     const int32_t *seq_lens, const float *mass, int32_t ld_mass, int32_t keep,
+                     int32_t sink, int32_t recent, const int32_t *dst_table, int32_t *kept,
+                     int32_t *new_lens, float *mass_out, void *ws, size_t ws_bytes,
+                     qsa_stream_t stream) {
+  QSA_RANGE("qsa_evict");
+  (void)ws;
+  (void)ws_bytes;
+  try {
+    QSA_TRY(check_dims(dims));
+    QSA_TRY(check_cache(cache, true, true));
+    if (B < 0 || B > 65535 || B > cache->num_seqs)
+      return fail(QSA_ERR_INVALID_ARG, "B=%d outside [0, 65535] or over the block_table rows %d", B,
+                  cache->num_seqs);
+    if (ld_mass <= 0 || ld_mass > (1 << 28))
+      return fail(QSA_ERR_UNSUPPORTED, "ld_mass=%d outside [1, 2^28]", ld_mass);
+    if (keep < 1 || keep > (1 << 28))
+      return fail(QSA_ERR_UNSUPPORTED, "keep=%d outside [1, 2^28]", keep);
+    if (sink < 0 || recent < 1 || (int64_t)sink + recent > keep)
+      return fail(QSA_ERR_INVALID_ARG, "sink=%d, recent=%d: need sink >= 0, recent >= 1, sink + "
+                  "recent <= keep=%d", sink, recent, keep);
+    if (B == 0) return ok();
+    if (seq_lens == nullptr || mass == nullptr || dst_table == nullptr || kept == nullptr ||
+        new_lens == nullptr || mass_out == nullptr)
+      return fail(QSA_ERR_INVALID_ARG, "an argument array is NULL");
+    if (mass == mass_out || seq_lens == new_lens || dst_table == cache->block_table)
+      return fail(QSA_ERR_INVALID_ARG, "mass_out, new_lens and dst_table must not alias inputs");
+    QSA_ERRWORD(err);
+    return cuda_status(launch_evict(*dims, *cache, B, seq_lens, mass, ld_mass, keep, sink, recent,
+                                    dst_table, kept, new_lens, mass_out, err,
+                                    reinterpret_cast<cudaStream_t>(stream)),
+                       "qsa_evict launch");
+  } catch (...) {
+    return fail(QSA_ERR_CUDA, "qsa_evict: internal exception");
+  }
+}
+
 qsa_status qsa_check_device_errors(qsa_stream_t stream, int32_t *flags) {
   QSA_RANGE("qsa_check_device_errors");
   try {

@@ -16,7 +16,8 @@ enum : unsigned {
   ERR_BT = 4u,       // block-table column out of range
   ERR_SEL = 8u,      // selected block id out of range
   ERR_LEN = 16u,     // sequence length out of range
-  ERR_TIMEOUT = 32u  // bounded wait gave up
+  ERR_TIMEOUT = 32u, // bounded wait gave up
+  ERR_POS = 64u      // rotation position out of range
 };
 
 __device__ __forceinline__ void raise_err(unsigned *err, unsigned bit) {

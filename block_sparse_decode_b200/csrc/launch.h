@@ -104,4 +104,29 @@ cudaError_t launch_prefill_index_score(const qsa_dims &d, const qsa_cache &c, in
 cudaError_t launch_merge(int R, int B, int Hq, int D, const float *o_part, const float *lse_part,
                          void *out, int out_is_bf16, float *lse_out, cudaStream_t st);
 
+// Norm and rotation of query and key heads (norm_rope.cu).
+cudaError_t launch_norm_rope(int N, int Hq, int Hk, int D, const int32_t *pos, const void *q,
+                             int64_t q_stride, const void *k, int64_t k_stride, const float *q_w,
+                             const float *k_w, float eps, const float *rope, int max_pos, int rot,
+                             int interleaved, void *q_out, void *k_out, unsigned *err,
+                             cudaStream_t st);
+
+// Dense attention of appended chunks over the paged cache (chunk_attention.cu).
+size_t chunk_attention_ws_bytes(const qsa_dims &d, int S, int Nq);
+cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
+                                   const int32_t *seq_lens, const int32_t *row_start, int Nq,
+                                   const void *q, void *out, int out_is_bf16, float *lse,
+                                   void *ws, unsigned *err, cudaStream_t st);
+
+// Attention weight per micro-block (attention_mass.cu) and eviction (evict.cu).
+size_t attention_mass_ws_bytes(const qsa_dims &d, int S, int Nq);
+cudaError_t launch_attention_mass(const qsa_dims &d, const qsa_cache &c, int S,
+                                  const int32_t *seq_lens, const int32_t *row_start, int Nq,
+                                  const void *q, const float *lse, const float *mass_in,
+                                  float *mass, int ld, void *ws, unsigned *err, cudaStream_t st);
+cudaError_t launch_evict(const qsa_dims &d, const qsa_cache &c, int B, const int32_t *seq_lens,
+                         const float *mass, int ld, int keep, int sink, int recent,
+                         const int32_t *dst_table, int32_t *kept, int32_t *new_lens,
+                         float *mass_out, unsigned *err, cudaStream_t st);
+
 }  // namespace qsa

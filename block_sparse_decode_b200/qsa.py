@@ -34,7 +34,9 @@ EXPORTS = ("qsa_version", "qsa_last_error", "qsa_append", "qsa_index_score",
            "qsa_select_owned", "qsa_check_device_errors",
            "qsa_prefill_index_score_workspace_size", "qsa_prefill_index_score",
            "qsa_prefill_sparse_decode", "qsa_sparse_prefill_workspace_size",
-           "qsa_sparse_prefill")
+           "qsa_sparse_prefill", "qsa_qk_norm_rope", "qsa_chunk_attention_workspace_size",
+           "qsa_chunk_attention", "qsa_attention_mass_workspace_size", "qsa_attention_mass",
+           "qsa_evict_workspace_size", "qsa_evict")
 
 
 class QsaError(RuntimeError):
@@ -69,6 +71,7 @@ def lib() -> ctypes.CDLL:
                           "`python -m block_sparse_decode_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
+    I64 = ctypes.c_int64
     DP, CP = ctypes.POINTER(_Dims), ctypes.POINTER(_Cache)
     sig = {
         "qsa_version": (I32, []),
@@ -94,6 +97,14 @@ def lib() -> ctypes.CDLL:
         "qsa_sparse_prefill_workspace_size": (SZ, [DP, I32, I32, I32, I32]),
         "qsa_sparse_prefill": (I32, [DP, CP, I32, P, P, I32, P, P, P, I32, I32, P, I32, P, P, P,
                                      P, P, SZ, P, I32, P, P]),
+        "qsa_qk_norm_rope": (I32, [I32, I32, I32, I32, P, P, I64, P, I64, P, P, F, P, I32, I32,
+                                   I32, P, P, P]),
+        "qsa_chunk_attention_workspace_size": (SZ, [DP, I32, I32]),
+        "qsa_chunk_attention": (I32, [DP, CP, I32, P, P, I32, P, P, I32, P, P, SZ, P]),
+        "qsa_attention_mass_workspace_size": (SZ, [DP, I32, I32]),
+        "qsa_attention_mass": (I32, [DP, CP, I32, P, P, I32, P, P, P, P, I32, P, SZ, P]),
+        "qsa_evict_workspace_size": (SZ, [I32, I32, I32]),
+        "qsa_evict": (I32, [DP, CP, I32, P, P, I32, I32, I32, I32, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -458,3 +469,201 @@ def sparse_prefill(dims: QsaDims, cache: QsaCache, seq_lens, row_start, q, q_idx
         _nbytes(buf.ws), _ptr(buf.out, None, "out"),
         1 if buf.out.dtype == torch.bfloat16 else 0, _ptr(buf.lse, torch.float32, "lse"),
         _stream(stream)))
+
+
+# ------------------------------------------------- dense path and eviction
+
+def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda",
+               inv_freq=None) -> torch.Tensor:
+    """The rotation table of qsa_qk_norm_rope: fp32 [max_pos, rot_dim], cos then
+    sin of pos * theta^(-2i / rot_dim) (or pos * inv_freq[i], for other
+    frequencies). Angles of far positions lose digits in 32 bits, so they are
+    computed in 64 and rounded once."""
+    if inv_freq is None:
+        i = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+        inv_freq = float(theta) ** (-2.0 * i / rot_dim)
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+    if tuple(f.shape) != (rot_dim // 2,):
+        raise ValueError(f"inv_freq must hold rot_dim / 2 = {rot_dim // 2} frequencies")
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat((a.cos(), a.sin()), 1).to(torch.float32)
+
+
+def _on_current_device(t, stream):
+    """The calls launch on the current device (or on the device of an explicit
+    stream, which the caller has made current)."""
+    if stream is None and t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _head_rows(t: torch.Tensor, name: str):
+    """(pointer, token stride) of bf16 [N, H, D] whose head rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a bf16 [N, heads, D] tensor")
+    N, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    return t.data_ptr(), int(t.stride(0)) if N > 1 else int(H * D)
+
+
+def qsa_qk_norm_rope(pos, q, k, q_weight, k_weight, eps: float, rope, q_out, k_out=None,
+                     interleaved: bool = False, stream=None):
+    """Per-head RMS norm and rotation: q [N, Hq, D], k [N, Hk, D] (or None) ->
+    q_out, k_out. q and k may be views with any token stride; q_weight /
+    k_weight None: no norm; rope (see rope_table) None: no rotation."""
+    N, Hq, D = (int(x) for x in q.shape)
+    _on_current_device(q, stream)
+    qp, qs = _head_rows(q, "q")
+    kp, ks, Hk = None, 0, 0
+    if k is not None:
+        if k.dim() != 3 or int(k.shape[0]) != N or int(k.shape[2]) != D:
+            raise ValueError("k must be [N, Hk, D] with q's N and D")
+        (kp, ks), Hk = _head_rows(k, "k"), int(k.shape[1])
+        _shape(k_out, (N, Hk, D), "k_out")
+    _shape(q_out, (N, Hq, D), "q_out")
+    _shape(pos, (N,), "pos")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _shape(t, (D,), name)
+    _check(lib().qsa_qk_norm_rope(
+        N, Hq, Hk, D, _ptr(pos, torch.int32, "pos"), qp, qs, kp, ks,
+        _ptr(q_weight, torch.float32, "q_weight"), _ptr(k_weight, torch.float32, "k_weight"),
+        float(eps), _ptr(rope, torch.float32, "rope"), 0 if rope is None else int(rope.shape[0]),
+        0 if rope is None else int(rope.shape[1]), 1 if interleaved else 0,
+        _ptr(q_out, torch.bfloat16, "q_out"),
+        _ptr(k_out, torch.bfloat16, "k_out") if Hk else None, _stream(stream)))
+
+
+def _shape(t, shape, name):
+    if t is None or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got "
+                         f"{None if t is None else tuple(t.shape)}")
+
+
+def _chunk_shapes(dims, seq_lens, row_start, q):
+    S, Nq = int(seq_lens.shape[0]), int(q.shape[0])
+    _shape(row_start, (S + 1,), "row_start")
+    _shape(q, (Nq, dims.Hq, dims.D), "q")
+    return S, Nq
+
+
+def qsa_chunk_attention_workspace_size(dims: QsaDims, S: int, Nq: int) -> int:
+    return int(lib().qsa_chunk_attention_workspace_size(ctypes.byref(dims.c()), S, Nq))
+
+
+def qsa_chunk_attention(dims: QsaDims, cache: QsaCache, seq_lens, row_start, q, out, lse=None,
+                        ws=None, stream=None):
+    """Dense causal attention of the chunk rows: q [Nq, Hq, D] -> out, lse [Nq, Hq]."""
+    S, Nq = _chunk_shapes(dims, seq_lens, row_start, q)
+    _on_current_device(q, stream)
+    _shape(out, (Nq, dims.Hq, dims.D), "out")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out must be bf16 or fp32")
+    if lse is not None:
+        _shape(lse, (Nq, dims.Hq), "lse")
+    _check(lib().qsa_chunk_attention(
+        ctypes.byref(dims.c()), ctypes.byref(cache.c()), S,
+        _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(row_start, torch.int32, "row_start"), Nq,
+        _ptr(q, torch.bfloat16, "q"), _ptr(out, None, "out"),
+        1 if out.dtype == torch.bfloat16 else 0, _ptr(lse, torch.float32, "lse"),
+        _ptr(ws, None, "ws"), _nbytes(ws), _stream(stream)))
+
+
+@dataclass
+class ChunkBuffers:
+    """Outputs and scratch of qsa_chunk_attention for fixed (S, Nq)."""
+
+    out: torch.Tensor   # bf16 or fp32 [Nq, Hq, D]
+    lse: torch.Tensor   # fp32 [Nq, Hq]
+    ws: torch.Tensor    # uint8 scratch
+
+
+def alloc_chunk_attention(dims: QsaDims, S: int, Nq: int, device="cuda",
+                          out_dtype=torch.bfloat16) -> ChunkBuffers:
+    ws_bytes = max(16, qsa_chunk_attention_workspace_size(dims, S, Nq))
+    return ChunkBuffers(
+        out=torch.empty((Nq, dims.Hq, dims.D), dtype=out_dtype, device=device),
+        lse=torch.empty((Nq, dims.Hq), dtype=torch.float32, device=device),
+        ws=torch.empty((ws_bytes,), dtype=torch.uint8, device=device))
+
+
+def qsa_attention_mass_workspace_size(dims: QsaDims, S: int, Nq: int) -> int:
+    return int(lib().qsa_attention_mass_workspace_size(ctypes.byref(dims.c()), S, Nq))
+
+
+def qsa_attention_mass(dims: QsaDims, cache: QsaCache, seq_lens, row_start, q, lse, mass_in, mass,
+                       ws=None, stream=None):
+    """mass [S, ld] = mass_in (None: 0) + the weight each micro-block got from
+    the chunk rows q [Nq, Hq, D] with their lse [Nq, Hq]."""
+    S, Nq = _chunk_shapes(dims, seq_lens, row_start, q)
+    _on_current_device(q, stream)
+    _shape(lse, (Nq, dims.Hq), "lse")
+    ld = int(mass.shape[1])
+    _shape(mass, (S, ld), "mass")
+    if mass_in is not None:
+        _shape(mass_in, (S, ld), "mass_in")
+    _check(lib().qsa_attention_mass(
+        ctypes.byref(dims.c()), ctypes.byref(cache.c()), S,
+        _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(row_start, torch.int32, "row_start"), Nq,
+        _ptr(q, torch.bfloat16, "q"), _ptr(lse, torch.float32, "lse"),
+        _ptr(mass_in, torch.float32, "mass_in"), _ptr(mass, torch.float32, "mass"), ld,
+        _ptr(ws, None, "ws"), _nbytes(ws), _stream(stream)))
+
+
+@dataclass
+class MassBuffers:
+    """Output and scratch of qsa_attention_mass for fixed (S, Nq, ld)."""
+
+    mass: torch.Tensor  # fp32 [S, ld]
+    ws: torch.Tensor    # uint8 scratch
+
+
+def alloc_attention_mass(dims: QsaDims, S: int, Nq: int, ld: int, device="cuda") -> MassBuffers:
+    ws_bytes = max(16, qsa_attention_mass_workspace_size(dims, S, Nq))
+    return MassBuffers(mass=torch.zeros((S, ld), dtype=torch.float32, device=device),
+                       ws=torch.empty((ws_bytes,), dtype=torch.uint8, device=device))
+
+
+def qsa_evict_workspace_size(B: int, ld_mass: int, keep: int) -> int:
+    return int(lib().qsa_evict_workspace_size(B, ld_mass, keep))
+
+
+def qsa_evict(dims: QsaDims, cache: QsaCache, seq_lens, mass, keep: int, sink: int, recent: int,
+              dst_table, kept, new_lens, mass_out, ws=None, stream=None):
+    """Keep `keep` micro-blocks of every sequence (the first `sink`, the last
+    `recent`, and the heaviest of the others), copied to dst_table's pages."""
+    B, ld = int(seq_lens.shape[0]), int(mass.shape[1])
+    _on_current_device(mass, stream)
+    _shape(mass, (B, ld), "mass")
+    _shape(mass_out, (B, ld), "mass_out")
+    _shape(kept, (B, int(keep)), "kept")
+    _shape(new_lens, (B,), "new_lens")
+    _shape(dst_table, (B, int(cache.block_table.shape[1])), "dst_table")
+    _check(lib().qsa_evict(
+        ctypes.byref(dims.c()), ctypes.byref(cache.c()), B,
+        _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(mass, torch.float32, "mass"), ld, int(keep),
+        int(sink), int(recent), _ptr(dst_table, torch.int32, "dst_table"),
+        _ptr(kept, torch.int32, "kept"), _ptr(new_lens, torch.int32, "new_lens"),
+        _ptr(mass_out, torch.float32, "mass_out"), _ptr(ws, None, "ws"), _nbytes(ws),
+        _stream(stream)))
+
+
+@dataclass
+class EvictBuffers:
+    """Outputs and scratch of qsa_evict for fixed (B, ld, keep)."""
+
+    kept: torch.Tensor      # int32 [B, keep]
+    new_lens: torch.Tensor  # int32 [B]
+    mass: torch.Tensor      # fp32 [B, ld]
+    ws: torch.Tensor        # uint8 scratch
+
+
+def alloc_evict(B: int, ld: int, keep: int, device="cuda") -> EvictBuffers:
+    ws_bytes = max(16, qsa_evict_workspace_size(B, ld, keep))
+    return EvictBuffers(kept=torch.empty((B, keep), dtype=torch.int32, device=device),
+                        new_lens=torch.empty((B,), dtype=torch.int32, device=device),
+                        mass=torch.empty((B, ld), dtype=torch.float32, device=device),
+                        ws=torch.empty((ws_bytes,), dtype=torch.uint8, device=device))

@@ -373,13 +373,127 @@ qsa_status qsa_sparse_prefill(const qsa_dims *dims, const qsa_cache *cache, int3
                               size_t ws_bytes, void *out, int32_t out_is_bf16,
                               float *lse_out, qsa_stream_t stream);
 
+/* ------------------------------------------------- dense path and eviction
+ * The calls around the sparse path: the norm and rotation before an append or
+ * an attention, dense attention of appended chunks (layers or contexts that
+ * do not select), and the eviction of the micro-blocks that received least
+ * attention. A serving loop calls them in this order: qsa_qk_norm_rope,
+ * qsa_append, qsa_chunk_attention, qsa_attention_mass and, when a context has
+ * grown past its budget, qsa_evict; after it the loop installs the
+ * destination table and goes on with any call over the shortened sequences.
+ * A key carries its rotation from when it was appended, so an evicted cache
+ * needs none again: a token's rotation position (qsa_qk_norm_rope) and its
+ * place in the cache (qsa_append's tok_pos) are then two numbers. */
+
+/* RMS norm of every query and key head, then the position rotation, in one
+ * pass; also for indexer queries and keys (D = di):
+ *   y = x * (sum x^2 / D + eps)^(-1/2) * w          per head
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
+ *   pos       int32 [N]: rotation position of each token; a token with
+ *             pos < 0 is padding, its output rows stay as they were
+ *   q, k      bf16: token n's heads are Hq (Hk) rows of D values from
+ *             q + n * q_stride (k + n * k_stride), strides in elements,
+ *             multiples of 8 (e.g. views of one fused projection output)
+ *   q_weight, k_weight  fp32 [D], or NULL: no norm for that tensor
+ *   rope      fp32 [max_pos, rot_dim]: cos of the rot_dim / 2 angles of a
+ *             position, then their sin. A token whose pos >= max_pos sets
+ *             QSA_ERR_BOUNDS (flag 64) and is skipped
+ *   rot_dim   values of a head that rotate, the first ones: a multiple of 16
+ *             in [0, D]; 0: no rotation (rope may be NULL)
+ *   interleaved  0: pairs (i, i + rot_dim / 2); else pairs (2i, 2i + 1)
+ *   q_out     bf16 [N, Hq, D]; k_out  bf16 [N, Hk, D]; each may be its input
+ *             where that is dense (stride = heads * D), and must not overlap
+ *             an input otherwise.
+ * Norm, weight and rotation are fp32, rounded to bf16 once. All arrays but
+ * pos are 16-byte aligned. Supported: D in {64, 128}; Hk = 0 (k and k_out
+ * NULL) handles queries alone. */
+qsa_status qsa_qk_norm_rope(int32_t N, int32_t Hq, int32_t Hk, int32_t D, const int32_t *pos,
+                            const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                            const float *q_weight, const float *k_weight, float eps,
+                            const float *rope, int32_t max_pos, int32_t rot_dim,
+                            int32_t interleaved, void *q_out, void *k_out, qsa_stream_t stream);
+
+/* Scratch bytes of qsa_chunk_attention. */
+size_t qsa_chunk_attention_workspace_size(const qsa_dims *dims, int32_t S, int32_t Nq);
+
+/* Dense causal attention of the rows of appended chunks over the paged cache.
+ *   seq_lens, row_start, Nq  the chunks, as in the sparse prefill above: row
+ *            i of sequence s sees its first L_s - T_s + i + 1 tokens. T_s = 1
+ *            is a decode token; T_s = 0 a sequence without rows
+ *   q        bf16 [Nq, Hq, D]
+ *   out      [Nq, Hq, D], bf16 if out_is_bf16 else fp32
+ *   lse_out  fp32 [Nq, Hq] (natural log) or NULL
+ *   ws       qsa_chunk_attention_workspace_size bytes, 16-byte aligned, no
+ *            initialisation needed; used until the call's kernels finish (two
+ *            calls that may run at the same time need two).
+ * Rows outside every chunk stay as they were. So do the rows of a chunk that
+ * overruns Nq, is longer than its sequence, or whose sequence is longer than
+ * max_pages_per_seq * P tokens; it raises device error flag 16. A page id out
+ * of range raises flag 2 and leaves the values of its sequence's rows
+ * undefined. The cache slots past L_s may hold anything; the K and V of
+ * tokens below L_s must be finite. 0 <= S, Nq <= 65535. */
+qsa_status qsa_chunk_attention(const qsa_dims *dims, const qsa_cache *cache, int32_t S,
+                               const int32_t *seq_lens, const int32_t *row_start, int32_t Nq,
+                               const void *q, void *out, int32_t out_is_bf16, float *lse_out,
+                               void *ws, size_t ws_bytes, qsa_stream_t stream);
+
+/* Scratch bytes of qsa_attention_mass. */
+size_t qsa_attention_mass_workspace_size(const qsa_dims *dims, int32_t S, int32_t Nq);
+
+/* The attention weight that the rows of the chunks gave to each micro-block:
+ *   mass[s][j] = mass_in[s][j] + sum over the tokens t of block j, the rows of
+ *                sequence s that see t, and the query heads h, of
+ *                e^(scale * q_h . K_t - lse_h)
+ *   seq_lens, row_start, Nq, q, ws  as in qsa_chunk_attention
+ *   lse      fp32 [Nq, Hq]: the rows' LSE (qsa_chunk_attention's lse_out). A
+ *            row and head with LSE = -inf gives nothing
+ *   mass_in  fp32 [S, ld_mass] or NULL (zeros);  mass  fp32 [S, ld_mass], may
+ *            be mass_in itself. All ld_mass entries of the S rows are written
+ *            (mass_in's value where no row sees a token of the block).
+ * The sums are fp32 in a fixed order: the same call gives the same bits. A
+ * chunk that qsa_chunk_attention would skip, or whose ceil(L_s / 4) blocks
+ * exceed ld_mass, adds nothing and raises device error flag 16. */
+qsa_status qsa_attention_mass(const qsa_dims *dims, const qsa_cache *cache, int32_t S,
+                              const int32_t *seq_lens, const int32_t *row_start, int32_t Nq,
+                              const void *q, const float *lse, const float *mass_in, float *mass,
+                              int32_t ld_mass, void *ws, size_t ws_bytes, qsa_stream_t stream);
+
+/* Scratch bytes of qsa_evict (0 for this implementation). */
+size_t qsa_evict_workspace_size(int32_t B, int32_t ld_mass, int32_t keep);
+
+/* Evict micro-blocks from B sequences by their accumulated weight. Of the
+ * nb = ceil(L_b / 4) blocks of a sequence n = min(keep, nb) stay: the first
+ * `sink`, the last `recent` (the trailing partial block is one of them), and
+ * of the others those with the largest mass (of equal ones the lowest index).
+ * The kept blocks are copied in ascending order to the destination pages:
+ * block i of the shortened sequence lies at tokens [4i, 4i + 4) of the pages
+ * of dst_table's row b, K, V, indexer keys and side-cache key alike. The
+ * source pages are not written; the caller frees them afterwards.
+ *   mass      fp32 [B, ld_mass] (first nb entries used; NaN ranks lowest)
+ *   dst_table int32 [B, max_pages_per_seq]: pages of the same pools. No page
+ *             of it may be a page of block_table that this call reads, nor
+ *             appear twice; entries past the kept blocks are not read
+ *   kept      int32 [B, keep]: the kept blocks' old indices, ascending, then -1
+ *   new_lens  int32 [B]: 4 n less what the trailing block lacks
+ *   mass_out  fp32 [B, ld_mass]: the kept blocks' mass in their new order,
+ *             then zeros (not mass itself)
+ *   ws        may be NULL when its size is 0.
+ * A sequence that is negative or longer than 4 * ld_mass tokens raises device
+ * error flag 16 and gets n = 0. Supported: 1 <= keep, sink >= 0, recent >= 1,
+ * sink + recent <= keep. */
+qsa_status qsa_evict(const qsa_dims *dims, const qsa_cache *cache, int32_t B,
+                     const int32_t *seq_lens, const float *mass, int32_t ld_mass, int32_t keep,
+                     int32_t sink, int32_t recent, const int32_t *dst_table, int32_t *kept,
+                     int32_t *new_lens, float *mass_out, void *ws, size_t ws_bytes,
+                     qsa_stream_t stream);
+
 /* Wait for `stream`, then read and clear the device error word of the
  * current device. *flags receives the bits that were set (0 if none):
  *   1 sequence row out of range    2 page id out of range
  *   4 block-table column out of range   8 selected block id out of range
  *   16 sequence length out of range (negative, or nb > ld_scores)
- *   32 a bounded wait gave up
- * Returns QSA_ERR_BOUNDS if any bit below 32 was set, QSA_ERR_TIMEOUT if only
+ *   32 a bounded wait gave up      64 rotation position out of range
+ * Returns QSA_ERR_BOUNDS if any bit but 32 was set, QSA_ERR_TIMEOUT if only
  * bit 32 was, QSA_OK otherwise. flags may be NULL. */
 qsa_status qsa_check_device_errors(qsa_stream_t stream, int32_t *flags);
 

@@ -1,0 +1,144 @@
+"""Refusals of the dense-path calls (no GPU needed: the checks run on the host,
+before any CUDA call), and the rotation table."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+from block_sparse_decode_b200 import build, qsa
+
+BAD, UNS = qsa.QSA_ERR_INVALID_ARG, qsa.QSA_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return qsa.lib()
+
+
+DIMS = dict(Hq=32, Hkv=4, D=128, Hi=16, di=128, P=64, scale=0.1)
+
+
+def dims(**kw):
+    return qsa._Dims(*{**DIMS, **kw}.values())
+
+
+def cache(k=16, table=16, num_seqs=4):
+    return qsa._Cache(k, 16, 16, 16, table, num_seqs, 8, 8)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(N=-1), BAD), (dict(Hq=0), BAD), (dict(Hk=-1), BAD), (dict(D=96), UNS),
+    (dict(rot=24), UNS), (dict(rot=144), UNS), (dict(rot=-16), UNS), (dict(eps=-1.0), BAD),
+    (dict(eps=math.nan), BAD), (dict(max_pos=0), BAD), (dict(q=None), BAD), (dict(k=None), BAD),
+    (dict(rope=None), BAD), (dict(pos=None), BAD), (dict(k_out=None), BAD), (dict(q=24), BAD),
+    (dict(q_stride=128), BAD), (dict(q_stride=4 * 128 + 4), BAD), (dict(k_stride=0), BAD),
+    (dict(qw=8), BAD), (dict(q_out=32, q=32, q_stride=1024), BAD),
+])
+def test_norm_rope_refusals(L, change, status):
+    a = dict(N=2, Hq=4, Hk=2, D=128, pos=16, q=16, q_stride=512, k=16, k_stride=256, qw=16, kw=16,
+             eps=1e-6, rope=16, max_pos=8, rot=128, pairs=0, q_out=32, k_out=32, stream=None)
+    assert L.qsa_qk_norm_rope(*{**a, **change}.values()) == status
+    assert L.qsa_last_error().decode()
+
+
+def test_norm_rope_of_nothing(L):
+    assert L.qsa_qk_norm_rope(0, 4, 0, 64, None, None, 0, None, 0, None, None, 0.0, None, 0, 0, 0,
+                              None, None, None) == qsa.QSA_OK
+
+
+CHUNK = dict(dims=dims(), cache=cache(), S=2, lens=16, start=16, Nq=5, q=16)
+
+
+def call(fn, a):
+    a = dict(a)
+    a["dims"], a["cache"] = ctypes.byref(a["dims"]), ctypes.byref(a["cache"])
+    return fn(*a.values())
+
+
+COMMON = [(dict(dims=dims(D=64)), UNS), (dict(dims=dims(Hkv=5)), BAD), (dict(dims=dims(P=6)), UNS),
+          (dict(dims=dims(Hkv=2)), UNS), (dict(cache=cache(k=17)), BAD),
+          (dict(cache=cache(table=None)), BAD), (dict(S=5), BAD), (dict(S=-1), BAD),
+          (dict(Nq=-1), BAD), (dict(Nq=65536), BAD), (dict(lens=None), BAD), (dict(start=None), BAD),
+          (dict(q=None), BAD), (dict(q=24), BAD)]
+
+
+@pytest.mark.parametrize("change,status", COMMON + [(dict(out=None), BAD), (dict(out=8), BAD),
+                                                    (dict(ws=8), BAD)])
+def test_chunk_attention_refusals(L, change, status):
+    a = dict(CHUNK, out=16, bf16=1, lse=None, ws=16, ws_bytes=1 << 40, stream=None)
+    assert call(L.qsa_chunk_attention, {**a, **change}) == status
+    assert L.qsa_last_error().decode()
+
+
+@pytest.mark.parametrize("change,status", COMMON + [(dict(lse=None), BAD), (dict(mass=None), BAD),
+                                                    (dict(ld=0), BAD), (dict(ws=8), BAD)])
+def test_attention_mass_refusals(L, change, status):
+    a = dict(CHUNK, lse=16, mass_in=None, mass=16, ld=64, ws=16, ws_bytes=1 << 40, stream=None)
+    assert call(L.qsa_attention_mass, {**a, **change}) == status
+    assert L.qsa_last_error().decode()
+
+
+def test_workspaces_are_asked_for(L):
+    d = qsa.QsaDims(*DIMS.values())
+    need = qsa.qsa_chunk_attention_workspace_size(d, 2, 5)
+    a = dict(CHUNK, out=16, bf16=1, lse=None, ws=16, ws_bytes=need - 1, stream=None)
+    if need:
+        assert call(L.qsa_chunk_attention, a) == BAD and b"workspace" in L.qsa_last_error()
+    need = qsa.qsa_attention_mass_workspace_size(d, 2, 5)
+    a = dict(CHUNK, lse=16, mass_in=None, mass=16, ld=64, ws=None, ws_bytes=need, stream=None)
+    if need:
+        assert call(L.qsa_attention_mass, a) == BAD and b"workspace" in L.qsa_last_error()
+    for f in (L.qsa_chunk_attention_workspace_size, L.qsa_attention_mass_workspace_size):
+        assert f(None, 2, 5) == 0 and f(ctypes.byref(dims()), 0, 5) == 0
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dims=dims(di=96)), UNS), (dict(cache=cache(k=None)), BAD), (dict(B=5), BAD),
+    (dict(B=-1), BAD), (dict(ld=0), UNS), (dict(keep=0), UNS), (dict(sink=-1), BAD),
+    (dict(recent=0), BAD), (dict(sink=5), BAD), (dict(lens=None), BAD), (dict(mass=None), BAD),
+    (dict(dst=None), BAD), (dict(kept=None), BAD), (dict(new=None), BAD), (dict(mass_out=None), BAD),
+    (dict(mass_out=32), BAD), (dict(new=16), BAD), (dict(dst=16), BAD),
+])
+def test_evict_refusals(L, change, status):
+    a = dict(dims=dims(), cache=cache(), B=2, lens=16, mass=32, ld=64, keep=8, sink=4, recent=4,
+             dst=48, kept=64, new=80, mass_out=96, ws=None, ws_bytes=0, stream=None)
+    assert call(L.qsa_evict, {**a, **change}) == status
+    assert L.qsa_last_error().decode()
+
+
+def test_calls_on_nothing(L):
+    a = dict(CHUNK, out=None, bf16=1, lse=None, ws=None, ws_bytes=0, stream=None)
+    assert call(L.qsa_chunk_attention, {**a, "S": 0}) == qsa.QSA_OK
+    assert call(L.qsa_chunk_attention, {**a, "Nq": 0}) == qsa.QSA_OK
+    a = dict(CHUNK, lse=None, mass_in=None, mass=None, ld=64, ws=None, ws_bytes=0, stream=None)
+    assert call(L.qsa_attention_mass, {**a, "S": 0}) == qsa.QSA_OK
+
+
+def test_rope_table():
+    t = qsa.rope_table(300, 64, 5e5, device="cpu")
+    assert t.shape == (300, 64) and t.dtype == torch.float32
+    for p, i in ((0, 0), (299, 31), (123, 7)):
+        a = p * 5e5 ** (-2 * i / 64)
+        assert abs(float(t[p, i]) - math.cos(a)) < 1e-7
+        assert abs(float(t[p, 32 + i]) - math.sin(a)) < 1e-7
+    u = qsa.rope_table(10, 4, inv_freq=[1.0, 0.5], device="cpu")
+    assert abs(float(u[9, 1]) - math.cos(4.5)) < 1e-7
+    with pytest.raises(ValueError):
+        qsa.rope_table(10, 4, inv_freq=[1.0], device="cpu")
+
+
+def test_binding_refusals():
+    bf = torch.bfloat16
+    q = torch.zeros((2, 3, 64), dtype=bf)
+    with pytest.raises(ValueError, match="CUDA"):
+        qsa.qsa_qk_norm_rope(torch.zeros(2, dtype=torch.int32), q, None, None, None, 0.0, None, q)
+    d = qsa.QsaDims(*DIMS.values())
+    with pytest.raises(ValueError, match="row_start"):
+        qsa.qsa_chunk_attention(d, None, torch.zeros(2, dtype=torch.int32),
+                                torch.zeros(2, dtype=torch.int32), q, q)
+    with pytest.raises(ValueError, match="q must have"):
+        qsa.qsa_attention_mass(d, None, torch.zeros(2, dtype=torch.int32),
+                               torch.zeros(3, dtype=torch.int32), q, None, None, None)
