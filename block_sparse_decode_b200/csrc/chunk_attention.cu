@@ -3,113 +3,958 @@
 //
 //   z_t = scale q.K_t for the row's len = L - T + i + 1 first tokens,
 //   LSE = ln sum e^(z_t), out = sum e^(z_t - LSE) V_t
-// One warp per (row, query head): 4 dims a lane, one token at a time, with
-// the running maximum and sum of the softmax in registers.
+//
+// Three kernels, chained by programmatic dependent launch:
+//   plan    one CTA: the list of groups (up to 2 * TT tokens of one chunk,
+//           TT = 128 / G) and the prefix of their work; an item is a group and
+//           a KV head, its steps the 128-token tiles of the cache that its
+//           last row sees;
+//   attend  one CTA per SM over an equal range of the flattened steps, so that
+//           one long sequence and many short ones fill the machine alike. An
+//           item that several CTAs share leaves partial results in the
+//           workspace;
+//   join    merges those by their LSEs.
+//
+// attend: the G query heads of a KV head share its K and V, so a tile of 128
+// MMA rows holds TT tokens x G heads. An item has two such tiles, one per
+// slot, that use the same K and V (a group of at most TT tokens has one: its
+// slots then take the odd and even steps, and are merged at the end). Per
+// step and slot S = Q K^T (M = N = K = 128), the softmax of S as bf16 P in
+// tensor memory over S itself, and O += P V, both tcgen05. While one slot's
+// warps work on its softmax, the tensor cores work for the other.
+//   warps 0-3, 4-7  softmax of slot 0, 1: a thread holds a row of S, so the
+//                   row's maximum and sum need no exchange
+//   warps 8-11      rescale O where a maximum grew; at an item's end read O
+//                   and write the result
+//   warp 12         issues the MMAs
+//   warp 13, 14     TMA of Q and K tiles; of V tiles, whose rows past L_s are
+//                   set to zero (0 * NaN in a stale slot would reach the sum)
+// The maximum is held in the exponent's unit (log2) and rounded up to a whole
+// number, so every rescaling is by a power of two and exact, and it is only
+// raised when it grew by more than 8 since O was last rescaled (P stays below
+// 256, the sums in fp32): few tiles rescale at all.
+// P is rounded to bf16 (2^-8 of a weight, as V's own precision), the row sum
+// adds the fp32 values.
+// Every mbarrier wait is bounded; after a timeout the roles stop, wait for
+// their copies and MMAs, and free the tensor memory.
+#include <cuda.h>
+
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
+#include "tc_util.cuh"
+#include "umma_desc.h"
 
 namespace qsa {
 namespace {
 
-struct ChunkArgs {
-  const __nv_bfloat16 *k_pool, *v_pool, *q;
+constexpr int CA_D = 128;
+constexpr int CA_KT = 128;  // cache tokens per step
+constexpr int CA_THREADS = 512;
+constexpr int CA_STAGES = 5;
+constexpr uint32_t CA_HALF = 128 * 128;  // bytes of 128 rows x 64 values
+constexpr uint32_t CA_TILE = 2 * CA_HALF;
+// control block, padded to the tiles' alignment, and the tiles: 227 KB exactly
+constexpr uint32_t CA_CTL = 3072;
+constexpr size_t CA_SMEM = CA_CTL + 2 * CA_TILE + CA_STAGES * CA_TILE;
+constexpr int CA_PLAN_THREADS = 1024;
+constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sums
+
+struct CaArgs {
   const int32_t *block_table, *seq_lens, *row_start;
+  int *hdr;          // [0] groups, [1] CTAs with work
+  long long *gpre;   // [Gmax + 1] prefix of the groups' units
+  int4 *ginfo;       // [2 Gmax] {seq, first row, tokens, steps}, {tokens its first row sees, L, -, -}
+  float *rec_lse;    // [CTAs][2][2][128]
+  float *rec_o;      // [CTAs][2][2][128][128]
   void *out;
   float *lse;
-  int S, Nq, Hq, Hkv, P, max_pages, num_pages, out_bf16;
+  int S, Nq, Gmax, Hq, Hkv, G, TT, P, box, max_pages, num_pages, out_bf16;
   float scale;
   unsigned *err;
 };
 
-__global__ void __launch_bounds__(256) chunk_attention_kernel(ChunkArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  pdl_wait();
-  const int r = (int)(w / a.Hq), h = (int)(w % a.Hq);
-  if (r >= a.Nq) return;
-  int lo = 0, hi = a.S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.row_start[mid] <= r) lo = mid; else hi = mid - 1;
+// ------------------------------------------------------------------ plan
+
+__device__ long long ca_scan(long long v, long long *wsum, long long *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  const int r0 = a.row_start[lo], r1 = a.row_start[lo + 1], L = a.seq_lens[lo];
-  if (r < r0 || r >= r1) return;
-  if (r0 < 0 || r1 > a.Nq || r1 - r0 > L || (long long)L > (long long)a.max_pages * a.P) {
-    if (lane == 0) raise_err(a.err, ERR_LEN);
+  if (lane == 31) wsum[warp] = x;
+  __syncthreads();
+  long long off = 0, tot = 0;
+  for (int i = 0; i < CA_PLAN_THREADS / 32; ++i) {
+    if (i < warp) off += wsum[i];
+    tot += wsum[i];
+  }
+  __syncthreads();
+  *total = tot;
+  return off + x - v;
+}
+
+// Units of one step: a step of two tiles counts twice that of one.
+__device__ __forceinline__ int ca_weight(int ntok, int TT) { return ntok > TT ? 2 : 1; }
+
+__global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int ctas) {
+  __shared__ long long wsum[CA_PLAN_THREADS / 32];
+  const int tid = threadIdx.x;
+  pdl_wait();
+  const int GT = 2 * a.TT;  // tokens of a group
+  long long gbase = 0;
+  for (int base = 0; base < a.S; base += CA_PLAN_THREADS) {
+    const int s = base + tid;
+    int ng = 0, r0 = 0, T = 0, L = 0;
+    if (s < a.S) {
+      r0 = a.row_start[s];
+      const int r1 = a.row_start[s + 1];
+      L = a.seq_lens[s];
+      T = r1 - r0;
+      if (r0 < 0 || r1 < r0 || r1 > a.Nq || T > L || (long long)L > (long long)a.max_pages * a.P)
+        raise_err(a.err, ERR_LEN);
+      else
+        ng = (T + GT - 1) / GT;
+    }
+    long long tot;
+    const long long off = gbase + ca_scan(ng, wsum, &tot);
+    for (int i = 0; i < ng; ++i) {
+      const long long g = off + i;
+      if (g >= a.Gmax) {  // only overlapping chunks can need more groups than rows allow
+        raise_err(a.err, ERR_LEN);
+        break;
+      }
+      const int ntok = min(GT, T - i * GT);
+      const int lim0 = L - T + i * GT + 1;
+      const int steps = (lim0 + ntok - 1 + CA_KT - 1) / CA_KT;
+      a.ginfo[2 * g] = make_int4(s, r0 + i * GT, ntok, steps);
+      a.ginfo[2 * g + 1] = make_int4(lim0, L, 0, 0);
+    }
+    gbase += tot;
+  }
+  const int G = (int)min(gbase, (long long)a.Gmax);
+  __syncthreads();
+  long long tbase = 0;
+  for (int base = 0; base < G; base += CA_PLAN_THREADS) {
+    const int g = base + tid;
+    long long n = 0;
+    if (g < G) {
+      const int4 gi = a.ginfo[2 * g];
+      n = (long long)a.Hkv * gi.w * ca_weight(gi.z, a.TT);
+    }
+    long long tot;
+    const long long off = tbase + ca_scan(n, wsum, &tot);
+    if (g < G) a.gpre[g] = off;
+    tbase += tot;
+  }
+  if (tid == 0) {
+    a.gpre[G] = tbase;
+    a.hdr[0] = G;
+    // every range holds at least two units, so every CTA inside an item's
+    // range has a step of it
+    a.hdr[1] = (int)min((long long)ctas, max(1LL, tbase / 2));
+  }
+}
+
+// ------------------------------------------------------------------ items
+
+__device__ __forceinline__ long long ca_bound(long long total, int c, int n) {
+  return total * c / n;
+}
+// The CTA whose range holds a unit.
+__device__ __forceinline__ int ca_owner(long long total, long long unit, int n) {
+  int c = (int)(unit * n / total);
+  while (c + 1 < n && ca_bound(total, c + 1, n) <= unit) ++c;
+  while (c > 0 && ca_bound(total, c, n) > unit) --c;
+  return c;
+}
+
+// The items of one CTA's range, in order. Every role walks them alike. Units
+// are counted from the range's start, which keeps them in 32 bits.
+struct CaWalk {
+  int u, hi;  // the item's first unit (before 0: it began in an earlier CTA), the range's end
+  int g, h, w;
+  int4 gi;  // {seq, first row, tokens, steps}
+  int lim0, L;
+  int a, b;  // this CTA's steps of the item
+  const CaArgs &p;
+
+  __device__ CaWalk(const CaArgs &args, int c) : p(args) {
+    const int n = p.hdr[1], G = p.hdr[0];
+    u = hi = g = h = 0;
+    w = 1;
+    if (G == 0 || c >= n) return;
+    const long long total = p.gpre[G], lo = ca_bound(total, c, n);
+    hi = (int)(ca_bound(total, c + 1, n) - lo);
+    int x = 0, y = G - 1;  // last group that starts at or before lo
+    while (x < y) {
+      const int m = (x + y + 1) >> 1;
+      if (p.gpre[m] <= lo) x = m; else y = m - 1;
+    }
+    g = x;
+    load();
+    const long long u0 = p.gpre[g], per = (long long)w * gi.w;
+    h = (int)((lo - u0) / per);
+    u = (int)(u0 + h * per - lo);
+  }
+  __device__ void load() {
+    gi = p.ginfo[2 * g];
+    const int4 m = p.ginfo[2 * g + 1];
+    lim0 = m.x;
+    L = m.y;
+    w = ca_weight(gi.z, p.TT);
+  }
+  // The steps [a, b) of the next item with any here (the range may start
+  // inside an item's last step); false when the range is done.
+  __device__ bool next(bool first) {
+    for (;;) {
+      if (!first) {
+        u += w * gi.w;
+        if (u >= hi) return false;
+        if (++h == p.Hkv) {
+          h = 0;
+          ++g;
+          load();
+        }
+      }
+      first = false;
+      if (u >= hi) return false;
+      a = u < 0 ? (-u + w - 1) / w : 0;
+      b = min(gi.w, (hi - u + w - 1) / w);
+      if (a < b) return true;
+    }
+  }
+  __device__ bool two() const { return w == 2; }
+  // Steps of slot 0's rows in a two-tile item (slot 1's are all of them).
+  __device__ int steps0() const { return two() ? (lim0 + p.TT - 1 + CA_KT - 1) / CA_KT : gi.w; }
+  // Whether slot s works on step j.
+  __device__ bool active(int s, int j, int n0) const {
+    return two() ? (s == 1 || j < n0) : ((j - a) & 1) == s;
+  }
+};
+
+// ------------------------------------------------------------------ attend
+
+struct CaCtrl {
+  uint64_t full[CA_STAGES], empty[CA_STAGES];
+  uint64_t qfull, qempty, vraw, drain;
+  uint64_t sfull[2], ready[2], corr[2], ofull[2];
+  uint32_t tmem;
+  int abort_flag;
+  int kissued, vissued, qissued;
+  __nv_bfloat16 sc[2][128];      // a row's rescaling, a power of two
+  float sum[2][128], mx[2][128];  // and at an item's end its sum and maximum (log2)
+};
+
+__device__ __forceinline__ float ca_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void ca_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void ca_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// D (tensor memory) += A (tensor memory) * B (shared memory)
+__device__ __forceinline__ void ca_mma_ts(uint32_t d, uint32_t a, uint64_t db, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(db), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void ca_tma_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                          int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// Whole-warp bounded wait: lane 0 polls.
+__device__ __forceinline__ bool ca_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                             unsigned *err) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  return ok;
+}
+
+// The pieces of a step's 128 tokens, one lane each: the page of this lane's
+// piece, -1 for a piece past L or a bad page.
+__device__ __forceinline__ int ca_piece_page(const CaArgs &p, int s, int L, int tok0, int lane) {
+  const int t = tok0 + lane * p.box;
+  if (lane * p.box >= CA_KT || t >= L) return -1;
+  const int page = __ldg(p.block_table + (size_t)s * p.max_pages + t / p.P);
+  if (page < 0 || page >= p.num_pages) {
+    raise_err(p.err, ERR_PAGE);
+    return -1;
+  }
+  return page;
+}
+
+__global__ void __launch_bounds__(CA_THREADS, 1)
+    ca_attend_kernel(const __grid_constant__ CUtensorMap q_map,
+                     const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, const CaArgs p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  static_assert(sizeof(CaCtrl) <= CA_CTL, "control block");
+  CaCtrl &ctl = *reinterpret_cast<CaCtrl *>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t q_s = smem_u32(smem_raw) + CA_CTL;
+  if (q_s & 1023u) {  // the swizzled tiles need it; the same for every CTA
+    if (threadIdx.x == 0) raise_err(p.err, ERR_TIMEOUT);
+    pdl_wait();
     return;
   }
-  const int len = L - (r1 - r0) + (r - r0) + 1;
-  const size_t row = (size_t)r * a.Hq + h;
-  const uint2 qv = *reinterpret_cast<const uint2 *>(a.q + row * 128 + lane * 4);
-  const float q0 = bf16lo(qv.x), q1 = bf16hi(qv.x), q2 = bf16lo(qv.y), q3 = bf16hi(qv.y);
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-  for (int t = 0; t < len; ++t) {
-    const int page = a.block_table[(size_t)lo * a.max_pages + t / a.P];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) raise_err(a.err, ERR_PAGE);
-      continue;
+  const uint32_t ring = q_s + 2 * CA_TILE;
+  const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
+  const uint32_t qfull = smem_u32(&ctl.qfull), qempty = smem_u32(&ctl.qempty);
+  const uint32_t vraw = smem_u32(&ctl.vraw), drain = smem_u32(&ctl.drain);
+  const uint32_t sfull = smem_u32(&ctl.sfull[0]), ready = smem_u32(&ctl.ready[0]);
+  const uint32_t corr = smem_u32(&ctl.corr[0]), ofull = smem_u32(&ctl.ofull[0]);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < CA_STAGES; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
     }
-    const size_t at = (((size_t)page * a.P + t % a.P) * a.Hkv + h / (a.Hq / a.Hkv)) * 128 + lane * 4;
-    const uint2 kv = *reinterpret_cast<const uint2 *>(a.k_pool + at);
-    const uint2 vv = *reinterpret_cast<const uint2 *>(a.v_pool + at);
-    float z = q0 * bf16lo(kv.x) + q1 * bf16hi(kv.x) + q2 * bf16lo(kv.y) + q3 * bf16hi(kv.y);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    z *= a.scale;
-    if (z > m) {
-      const float f = __expf(m - z);
-      l *= f; o0 *= f; o1 *= f; o2 *= f; o3 *= f;
-      m = z;
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    mbar_init(vraw, 1);
+    mbar_init(drain, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(sfull + 8 * s, 1);
+      mbar_init(ready + 8 * s, 8);  // 4 softmax and 4 correction warps
+      mbar_init(corr + 8 * s, 4);
+      mbar_init(ofull + 8 * s, 1);
     }
-    const float p = __expf(z - m);
-    l += p;
-    o0 = fmaf(p, bf16lo(vv.x), o0); o1 = fmaf(p, bf16hi(vv.x), o1);
-    o2 = fmaf(p, bf16lo(vv.y), o2); o3 = fmaf(p, bf16hi(vv.y), o3);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    ctl.abort_flag = 0;
+    ctl.kissued = ctl.vissued = ctl.qissued = 0;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  o0 *= inv; o1 *= inv; o2 *= inv; o3 *= inv;
-  if (a.out_bf16)
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * 128 + lane * 4) =
-        make_uint2(pack_bf16x2(o0, o1), pack_bf16x2(o2, o3));
-  else
-    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * 128 + lane * 4) =
-        make_float4(o0, o1, o2, o3);
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&ctl.tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  volatile int *abort_flag = &ctl.abort_flag;
+  const float sl2 = p.scale * 1.4426950408889634f;
+  pdl_wait();
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const int s = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t ts = tmem + (uint32_t)(s * 128) + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c2 = sl2 > 0.f ? sl2 : 1.f;
+    uint32_t sph = 0, oph = 0;
+    CaWalk it(p, blockIdx.x);
+    bool ok = true;
+    for (bool more = it.next(true); more && ok; more = it.next(false)) {
+      const int n0 = it.steps0();
+      const int tok = (it.two() ? s * p.TT : 0) + r / p.G;
+      const bool valid = r < p.TT * p.G && tok < it.gi.z;
+      const int lim = valid ? it.lim0 + tok : 0;
+      const bool live = __any_sync(0xffffffffu, valid);
+      float m = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int j = it.a; j < it.b; ++j) {
+        if (!it.active(s, j, n0)) continue;
+        ok = ca_wait_warp(sfull + 8 * s, sph, abort_flag, p.err);
+        if (!ok) break;
+        sph ^= 1u;
+        tc_fence_after();
+        if (live) {
+          float v[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            tc_ld32_nowait(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+          tc_wait_ld();
+          if (!(sl2 > 0.f)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) v[i] *= sl2;
+          }
+          const int nv = lim - j * CA_KT;  // this row's tokens of the tile
+          if (__any_sync(0xffffffffu, nv < CA_KT)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= nv) v[i] = -INFINITY;
+          }
+          float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+#pragma unroll
+          for (int i = 4; i < 128; i += 4) {
+            t0 = fmaxf(t0, v[i]);
+            t1 = fmaxf(t1, v[i + 1]);
+            t2 = fmaxf(t2, v[i + 2]);
+            t3 = fmaxf(t3, v[i + 3]);
+          }
+          const float mt = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+          float f = 1.f;
+          const float mt2 = ceilf(mt * c2);
+          if (mt2 > m + CA_LAZY || m == -INFINITY) {
+            f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
+            m = fmaxf(m, mt2);
+          }
+          if (any) {
+            ctl.sc[s][r] = __float2bfloat16_rn(f);
+            l *= f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(corr + 8 * s);
+          }
+          const float off = m == -INFINITY ? 0.f : m;
+          uint32_t pk[64];
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 128; i += 4) {
+            const float e0 = ca_ex2(fmaf(v[i], c2, -off)), e1 = ca_ex2(fmaf(v[i + 1], c2, -off));
+            const float e2 = ca_ex2(fmaf(v[i + 2], c2, -off));
+            const float e3 = ca_ex2(fmaf(v[i + 3], c2, -off));
+            l0 += e0;
+            l1 += e1;
+            l2 += e2;
+            l3 += e3;
+            pk[i / 2] = pack_bf16x2(e0, e1);
+            pk[i / 2 + 1] = pack_bf16x2(e2, e3);
+          }
+          ca_st32(ts, pk);
+          ca_st32(ts + 32, pk + 32);
+          l += (l0 + l1) + (l2 + l3);
+          ca_wait_st();
+        } else if (any) {
+          ctl.sc[s][r] = __float2bfloat16_rn(1.f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(corr + 8 * s);
+        }
+        any = true;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready + 8 * s);
+      }
+      if (!ok) break;
+      if (any) {  // the item's maximum and sum, for its end
+        // (its last product had the correction warps' arrival, which follows
+        // their reading of the item before)
+        ok = ca_wait_warp(ofull + 8 * s, oph, abort_flag, p.err);
+        if (!ok) break;
+        oph ^= 1u;
+        ctl.sum[s][r] = l;
+        ctl.mx[s][r] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(corr + 8 * s);
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------- correction and results
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t to = tmem + 256u + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t cph[2] = {0, 0}, oph[2] = {0, 0};
+    CaWalk it(p, blockIdx.x);
+    bool ok = true;
+    for (bool more = it.next(true); more && ok; more = it.next(false)) {
+      const int n0 = it.steps0();
+      bool any[2] = {false, false};
+      for (int j = it.a; j < it.b && ok; ++j) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || !it.active(s, j, n0)) continue;
+          if (any[s]) {
+            ok = ca_wait_warp(corr + 8 * s, cph[s], abort_flag, p.err);
+            if (!ok) continue;
+            cph[s] ^= 1u;
+            const float f = __bfloat162float(ctl.sc[s][r]);
+            if (__any_sync(0xffffffffu, f != 1.f)) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tc_ld32_nowait(to + s * 128 + 32 * c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                ca_st32(to + s * 128 + 32 * c, o);
+              }
+              ca_wait_st();
+            }
+          }
+          any[s] = true;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready + 8 * s);
+        }
+      }
+      if (!ok) break;
+      // the end of the item: wait for its last products and sums
+      float l[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!any[s] || !ok) continue;
+        ok = ca_wait_warp(corr + 8 * s, cph[s], abort_flag, p.err) &&
+             ca_wait_warp(ofull + 8 * s, oph[s], abort_flag, p.err);
+        cph[s] ^= 1u;
+        oph[s] ^= 1u;
+        if (!ok) continue;
+        l[s] = ctl.sum[s][r];
+        m[s] = ctl.mx[s][r];
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = it.a == 0 && it.b == it.gi.w;
+      const int piece = it.a == 0 ? 1 : 0;  // record of a partial result
+      const bool two = it.two();
+#pragma unroll 1
+      for (int s = 0; s < (two ? 2 : 1); ++s) {
+        const int tok = s * p.TT + r / p.G;
+        const bool valid = r < p.TT * p.G && tok < it.gi.z;
+        if (!__any_sync(0xffffffffu, valid)) continue;
+        // weights of the slot's O (two tiles), or of both slots' (one tile)
+        float f0 = 0.f, f1 = 0.f, lse = -INFINITY;
+        if (two) {
+          const float ls = s == 0 ? l[0] : l[1], ms = s == 0 ? m[0] : m[1];
+          if (ls > 0.f) {
+            f0 = 1.f / ls;
+            lse = (ms + log2f(ls)) * 0.6931471805599453f;
+          }
+        } else {
+          const float M = fmaxf(l[0] > 0.f ? m[0] : -INFINITY, l[1] > 0.f ? m[1] : -INFINITY);
+          const float e0 = l[0] > 0.f ? ca_ex2(m[0] - M) : 0.f;
+          const float e1 = l[1] > 0.f ? ca_ex2(m[1] - M) : 0.f;
+          const float sum = e0 * l[0] + e1 * l[1];
+          if (sum > 0.f) {
+            f0 = e0 / sum;
+            f1 = e1 / sum;
+            lse = (M + log2f(sum)) * 0.6931471805599453f;
+          }
+        }
+        const bool has = two ? (s == 0 ? any[0] : any[1]) : true;
+        const bool has1 = !two && any[1];
+        const size_t row = (size_t)(it.gi.y + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
+        const size_t rec = ((size_t)blockIdx.x * 2 + piece) * 256 + s * 128 + r;
+        if (valid) {
+          if (!whole) p.rec_lse[rec] = lse;
+          else if (p.lse != nullptr) p.lse[row] = lse;
+        }
+        if (!has) continue;
+        const uint32_t ta = to + (two ? s * 128 : 0);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tc_ld32_nowait(ta + 32 * c, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = f0 > 0.f ? __float_as_uint(__uint_as_float(o[i]) * f0) : 0u;
+          if (has1) {
+            uint32_t o1[32];
+            tc_ld32_nowait(to + 128 + 32 * c, o1);
+            tc_wait_ld();
+            if (f1 > 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
+            }
+          }
+          if (!valid) continue;
+          if (whole && p.out_bf16) {
+            uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D +
+                                                 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]),
+                                   __uint_as_float(o[8 * i + 2 * k + 1]));
+              d[i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          } else {
+            uint4 *d = reinterpret_cast<uint4 *>(
+                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              d[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 12) {
+      // -------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t IDESC_S = f16_idesc(128, 128);
+        constexpr uint32_t IDESC_O = f16_idesc(128, 128) | (1u << 16);  // B = V: MN-major
+        CaWalk it(p, blockIdx.x);
+        uint32_t qph = 0, rph[2] = {0, 0};
+        int cnt = 0;  // steps before the current item
+        bool ok = true;
+        for (bool more = it.next(true); more && ok; more = it.next(false)) {
+          const int n0 = it.steps0();
+          const bool two = it.two();
+          const int stride = two ? 1 : 2;
+          auto scores = [&](int s, int j) -> bool {  // S_s = Q_s K_j^T
+            const int pos = 2 * (cnt + j - it.a), st = pos % CA_STAGES;
+            if (!mbar_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err))
+              return false;
+            tc_fence_after();
+            const uint64_t da = sw128_desc(q_s + (two ? s * CA_TILE : 0));
+            const uint64_t db = sw128_desc(ring + st * CA_TILE);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint64_t o = (uint64_t)(((k >> 2) * CA_HALF + (k & 3) * 32) >> 4);
+              tc_mma(tmem + s * 128, da + o, db + o, IDESC_S, k > 0 ? 1u : 0u);
+            }
+            tc_commit(sfull + 8 * s);
+            if (!two || s == 1) tc_commit(empty0 + 8 * st);  // the tile's last use
+            // the item's last scores free the query tiles
+            if (two ? (s == 1 && j == it.b - 1) : j == it.b - 1) tc_commit(qempty);
+            return true;
+          };
+          ok = mbar_wait(qfull, qph, abort_flag, p.err);
+          if (!ok) break;
+          qph ^= 1u;
+          bool began[2] = {false, false};
+          for (int s = 0; s < 2 && ok; ++s) {
+            const int j = two ? it.a : it.a + s;
+            if (j < it.b && it.active(s, j, n0)) ok = scores(s, j);
+          }
+          for (int j = it.a; j < it.b && ok; ++j) {
+            for (int s = 0; s < 2 && ok; ++s) {
+              if (!it.active(s, j, n0)) continue;
+              ok = mbar_wait(ready + 8 * s, rph[s], abort_flag, p.err);
+              if (!ok) break;
+              rph[s] ^= 1u;
+              const int pos = 2 * (cnt + j - it.a) + 1, st = pos % CA_STAGES;
+              ok = mbar_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err);
+              if (!ok) break;
+              tc_fence_after();
+              // V: 64-value halves CA_HALF apart (leading offset), 8-token
+              // groups 1024 bytes apart
+              const uint64_t db = (sw128_desc(ring + st * CA_TILE) & ~(0x3fffull << 16)) |
+                                  ((uint64_t)(CA_HALF >> 4) << 16);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                ca_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k,
+                          db + (uint64_t)((k * 2048) >> 4), IDESC_O, began[s] || k > 0 ? 1u : 0u);
+              began[s] = true;
+              if (!two || s == 1) tc_commit(empty0 + 8 * st);
+              const int jn = j + stride;
+              if (jn < it.b && it.active(s, jn, n0)) ok = scores(s, jn);
+              else tc_commit(ofull + 8 * s);  // the slot's last product
+            }
+          }
+          cnt += it.b - it.a;
+        }
+        if (!ok) {  // gave up: wait for what was issued
+          tc_commit(drain);
+          mbar_wait(drain, 0, abort_flag, p.err, TC_DRAIN_LIMIT, false);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // ------------------------------------------------------------ Q and K tiles
+      CaWalk it(p, blockIdx.x);
+      uint32_t qph = 0;
+      int cnt = 0, nq = 0;
+      bool ok = true;
+      for (bool more = it.next(true); more && ok; more = it.next(false)) {
+        if (nq > 0) {
+          ok = ca_wait_warp(qempty, qph, abort_flag, p.err);
+          if (!ok) break;
+          qph ^= 1u;
+        }
+        if (lane == 0) {
+          const int tiles = it.two() ? 2 : 1;
+          mbar_arrive_expect(qfull, (uint32_t)(tiles * 2 * p.TT * p.G * 128));
+          for (int s = 0; s < tiles; ++s)
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(q_s + s * CA_TILE + h * CA_HALF, &q_map, qfull, h * 64, it.h * p.G,
+                          it.gi.y + s * p.TT);
+        }
+        ++nq;
+        int page = ca_piece_page(p, it.gi.x, it.L, it.a * CA_KT, lane);
+        for (int j = it.a; j < it.b; ++j, ++cnt) {
+          int np = -1;
+          if (j + 1 < it.b) np = ca_piece_page(p, it.gi.x, it.L, (j + 1) * CA_KT, lane);
+          const int pos = 2 * cnt, st = pos % CA_STAGES;
+          ok = ca_wait_warp(empty0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1) ^ 1u, abort_flag,
+                            p.err);
+          if (!ok) break;
+          const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+          const uint32_t dst = ring + st * CA_TILE, bar = full0 + 8 * st;
+          if (lane == 0) mbar_arrive_expect(bar, (uint32_t)(__popc(live) * p.box * 256));
+          __syncwarp();
+          if (page >= 0) {
+            const int slot = (j * CA_KT + lane * p.box) % p.P;
+            for (int h = 0; h < 2; ++h)
+              ca_tma_4d(dst + h * CA_HALF + lane * p.box * 128, &k_map, bar, h * 64, it.h, slot,
+                        page);
+          }
+          page = np;
+        }
+      }
+      if (lane == 0) {
+        ctl.kissued = cnt;
+        ctl.qissued = nq;
+      }
+    } else if (warp == 14) {
+      // ------------------------------------------------------------------ V tiles
+      CaWalk it(p, blockIdx.x);
+      uint32_t vph = 0;
+      int cnt = 0;
+      bool ok = true;
+      for (bool more = it.next(true); more && ok; more = it.next(false)) {
+        int page = ca_piece_page(p, it.gi.x, it.L, it.a * CA_KT, lane);
+        for (int j = it.a; j < it.b; ++j, ++cnt) {
+          int np = -1;
+          if (j + 1 < it.b) np = ca_piece_page(p, it.gi.x, it.L, (j + 1) * CA_KT, lane);
+          const int pos = 2 * cnt + 1, st = pos % CA_STAGES;
+          ok = ca_wait_warp(empty0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1) ^ 1u, abort_flag,
+                            p.err);
+          if (!ok) break;
+          const int nrow = it.L - j * CA_KT;  // the tile's rows that hold tokens
+          const bool tail = nrow < CA_KT;
+          const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+          const uint32_t dst = ring + st * CA_TILE, bar = tail ? vraw : full0 + 8 * st;
+          if (lane == 0) mbar_arrive_expect(bar, (uint32_t)(__popc(live) * p.box * 256));
+          __syncwarp();
+          if (page >= 0) {
+            const int slot = (j * CA_KT + lane * p.box) % p.P;
+            for (int h = 0; h < 2; ++h)
+              ca_tma_4d(dst + h * CA_HALF + lane * p.box * 128, &v_map, bar, h * 64, it.h, slot,
+                        page);
+          }
+          if (tail) {
+            // (its own copies: waited for even after another role gave up)
+            bool in = true;
+            if (lane == 0) in = mbar_wait(vraw, vph, abort_flag, p.err, TC_SPIN_LIMIT, false);
+            ok = __shfl_sync(0xffffffffu, in, 0);
+            vph ^= 1u;
+            if (!ok) break;
+            for (int i = nrow * 8 + lane; i < CA_KT * 8; i += 32)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + h * CA_HALF +
+                                                                              i * 16),
+                             "r"(0)
+                             : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full0 + 8 * st);
+          }
+          page = np;
+        }
+      }
+      if (lane == 0) ctl.vissued = cnt;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  pdl_trigger();
+  if (ctl.abort_flag && threadIdx.x == 0) {
+    // copies that were issued: each stage's last one, and the last query tiles
+    for (int back = 0; back < CA_STAGES; ++back) {
+      const int k = ctl.kissued - 1 - back, v = ctl.vissued - 1 - back;
+      if (k >= 0 && back <= CA_STAGES / 2)
+        mbar_wait(full0 + 8 * ((2 * k) % CA_STAGES), (uint32_t)((2 * k / CA_STAGES) & 1),
+                  abort_flag, p.err, TC_DRAIN_LIMIT, false);
+      if (v >= 0 && back <= CA_STAGES / 2)
+        mbar_wait(full0 + 8 * ((2 * v + 1) % CA_STAGES), (uint32_t)(((2 * v + 1) / CA_STAGES) & 1),
+                  abort_flag, p.err, TC_DRAIN_LIMIT, false);
+    }
+    if (ctl.qissued > 0)
+      mbar_wait(qfull, (uint32_t)((ctl.qissued - 1) & 1), abort_flag, p.err, TC_DRAIN_LIMIT, false);
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ join
+
+// One block per CTA of the attend kernel: the item that started there and went
+// on in the next ones, one warp per row.
+__global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
+  pdl_wait();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int G = p.hdr[0], n = p.hdr[1];
+  if (G == 0 || c0 + 1 >= n) return;
+  const long long total = p.gpre[G];
+  const long long end = ca_bound(total, c0 + 1, n);
+  int x = 0, y = G - 1;  // the group that holds the unit before the range's end
+  while (x < y) {
+    const int m = (x + y + 1) >> 1;
+    if (p.gpre[m] <= end - 1) x = m; else y = m - 1;
+  }
+  const int4 gi = p.ginfo[2 * x];
+  const int w = ca_weight(gi.z, p.TT);
+  const long long per = (long long)w * gi.w;
+  const int h = (int)((end - 1 - p.gpre[x]) / per);
+  const long long u0 = p.gpre[x] + h * per;
+  if (u0 < ca_bound(total, c0, n)) return;  // began in an earlier CTA
+  const int c1 = ca_owner(total, u0 + (long long)w * (gi.w - 1), n);
+  if (c1 == c0) return;
+  const int rows = gi.z * p.G, per_tile = p.TT * p.G;
+  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += 8 * gridDim.y) {
+    const int at = i < per_tile ? i : 128 + i - per_tile;
+    auto rec = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * 256 + at; };
+    float M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.rec_lse + rec(c)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (M > -INFINITY) {
+      for (int c = c0; c <= c1; c += 4) {
+        float f[4];
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f[u] = c + u <= c1 ? __expf(__ldcg(p.rec_lse + rec(c + u)) - M) : 0.f;
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (f[u] > 0.f)
+            v[u] = __ldcg(reinterpret_cast<const float4 *>(p.rec_o + rec(c + u) * CA_D) + lane);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          sum += f[u];
+          acc.x = fmaf(f[u], v[u].x, acc.x);
+          acc.y = fmaf(f[u], v[u].y, acc.y);
+          acc.z = fmaf(f[u], v[u].z, acc.z);
+          acc.w = fmaf(f[u], v[u].w, acc.w);
+        }
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const size_t row = (size_t)(gi.y + i / p.G) * p.Hq + (size_t)h * p.G + i % p.G;
+    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+    if (p.out_bf16)
+      reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D)[lane] =
+          make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    else
+      reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * CA_D)[lane] = acc;
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = sum > 0.f ? M + logf(sum) : -INFINITY;
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+struct CaLayout {
+  size_t gpre, ginfo, lse, o, bytes;
+  int Gmax, TT, ctas;
+};
+
+CaLayout ca_layout(const qsa_dims &d, int S, int Nq) {
+  CaLayout l;
+  l.TT = 128 / (d.Hq / d.Hkv);
+  l.Gmax = S + Nq / (2 * l.TT);
+  l.ctas = device_sm_count();
+  auto r = [](size_t x) { return (x + 255) / 256 * 256; };
+  l.gpre = 256;
+  l.ginfo = l.gpre + r(8 * ((size_t)l.Gmax + 1));
+  l.lse = l.ginfo + r(32 * (size_t)l.Gmax);
+  l.o = l.lse + r((size_t)l.ctas * 512 * 4);
+  l.bytes = l.o + (size_t)l.ctas * 512 * CA_D * 4;
+  return l;
 }
 
 }  // namespace
 
 size_t chunk_attention_ws_bytes(const qsa_dims &d, int S, int Nq) {
-  (void)d; (void)S; (void)Nq;
-  return 0;
+  return ca_layout(d, S, Nq).bytes;
 }
 
 cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
                                    const int32_t *seq_lens, const int32_t *row_start, int Nq,
                                    const void *q, void *out, int out_is_bf16, float *lse,
                                    void *ws, unsigned *err, cudaStream_t st) {
-  (void)ws;
-  ChunkArgs a;
-  a.k_pool = static_cast<const __nv_bfloat16 *>(c.k_pool);
-  a.v_pool = static_cast<const __nv_bfloat16 *>(c.v_pool);
-  a.q = static_cast<const __nv_bfloat16 *>(q);
+  cudaError_t e;
+  EncodeTiledFn enc = encode_tiled_fn(&e);
+  if (e != cudaSuccess) return e;
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const CaLayout l = ca_layout(d, S, Nq);
+  char *w = static_cast<char *>(ws);
+  CaArgs a;
   a.block_table = c.block_table;
   a.seq_lens = seq_lens;
   a.row_start = row_start;
+  a.hdr = reinterpret_cast<int *>(w);
+  a.gpre = reinterpret_cast<long long *>(w + l.gpre);
+  a.ginfo = reinterpret_cast<int4 *>(w + l.ginfo);
+  a.rec_lse = reinterpret_cast<float *>(w + l.lse);
+  a.rec_o = reinterpret_cast<float *>(w + l.o);
   a.out = out;
   a.lse = lse;
   a.S = S;
   a.Nq = Nq;
+  a.Gmax = l.Gmax;
   a.Hq = d.Hq;
   a.Hkv = d.Hkv;
+  a.G = d.Hq / d.Hkv;
+  a.TT = l.TT;
   a.P = d.P;
+  a.box = std::min(d.P & -d.P, CA_KT);  // a piece never crosses a page
   a.max_pages = c.max_pages_per_seq;
   a.num_pages = c.num_pages;
   a.out_bf16 = out_is_bf16;
   a.scale = d.scale;
   a.err = err;
-  const long long warps = (long long)Nq * d.Hq;
-  return launch_pdl(chunk_attention_kernel, (unsigned)((warps + 7) / 8), 256, 0, st, a);
+
+  CUtensorMap q_map, k_map, v_map;
+  const cuuint32_t ones[4] = {1u, 1u, 1u, 1u};
+  {
+    const cuuint64_t dims[3] = {CA_D, (cuuint64_t)d.Hq, (cuuint64_t)Nq};
+    const cuuint64_t strides[2] = {CA_D * 2, (cuuint64_t)d.Hq * CA_D * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)a.G, (cuuint32_t)a.TT};
+    if (enc(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
+            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t row = (cuuint64_t)d.Hkv * CA_D * 2;
+    const cuuint64_t dims[4] = {CA_D, (cuuint64_t)d.Hkv, (cuuint64_t)d.P, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {CA_D * 2, row, row * d.P};
+    const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)a.box, 1u};
+    if (enc(i == 0 ? &k_map : &v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            i == 0 ? c.k_pool : c.v_pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  e = launch_pdl(ca_plan_kernel, 1, CA_PLAN_THREADS, 0, st, a, l.ctas);
+  if (e != cudaSuccess) return e;
+  e = ensure_dynamic_smem(reinterpret_cast<const void *>(ca_attend_kernel), CA_SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(ca_attend_kernel, l.ctas, CA_THREADS, CA_SMEM, st, q_map, k_map, v_map, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(ca_join_kernel, dim3(l.ctas, 4), 256, 0, st, a);
 }
 
 }  // namespace qsa
