@@ -29,6 +29,7 @@
 //   warp 12         issues the MMAs
 //   warp 13, 14     TMA of Q and K tiles; of V tiles, whose rows past L_s are
 //                   set to zero (0 * NaN in a stale slot would reach the sum)
+//   warp 15         announces the items to the other warps, a few ahead
 // The maximum is held in the exponent's unit (log2) and rounded up to a whole
 // number, so every rescaling is by a power of two and exact, and it is only
 // raised when it grew by more than 8 since O was last rescaled (P stays below
@@ -53,6 +54,8 @@ constexpr int CA_D = 128;
 constexpr int CA_KT = 128;  // cache tokens per step
 constexpr int CA_THREADS = 512;
 constexpr int CA_STAGES = 5;
+constexpr int CA_ITEMS = 4;     // items announced ahead
+constexpr int CA_READERS = 15;  // warps that read them
 constexpr uint32_t CA_HALF = 128 * 128;  // bytes of 128 rows x 64 values
 constexpr uint32_t CA_TILE = 2 * CA_HALF;
 // control block, padded to the tiles' alignment, and the tiles: 227 KB exactly
@@ -172,8 +175,8 @@ __device__ __forceinline__ int ca_owner(long long total, long long unit, int n) 
   return c;
 }
 
-// The items of one CTA's range, in order. Every role walks them alike. Units
-// are counted from the range's start, which keeps them in 32 bits.
+// The items of one CTA's range, in order. Units are counted from the range's
+// start, which keeps them in 32 bits.
 struct CaWalk {
   int u, hi;  // the item's first unit (before 0: it began in an earlier CTA), the range's end
   int g, h, w;
@@ -227,14 +230,20 @@ struct CaWalk {
       if (a < b) return true;
     }
   }
-  __device__ bool two() const { return w == 2; }
-  // Steps of slot 0's rows in a two-tile item (slot 1's are all of them).
-  __device__ int steps0() const { return two() ? (lim0 + p.TT - 1 + CA_KT - 1) / CA_KT : gi.w; }
-  // Whether slot s works on step j.
-  __device__ bool active(int s, int j, int n0) const {
-    return two() ? (s == 1 || j < n0) : ((j - a) & 1) == s;
-  }
 };
+
+// An item as the roles see it: this CTA's steps [a, b), none at the end of the
+// range. Slot 0's rows of a two-tile item see its steps below n0; a one-tile
+// item (n0 = -1) has its steps in turn on slot 0 and slot 1.
+struct __align__(16) CaItem {
+  int a, b, n0, ntok;
+  int h, row0, lim0, whole;
+  int seq, L, pad0, pad1;
+  __device__ bool two() const { return n0 >= 0; }
+};
+__device__ __forceinline__ bool ca_active(int s, int j, int a, int n0) {
+  return n0 >= 0 ? (s == 1 || j < n0) : ((j - a) & 1) == s;
+}
 
 // ------------------------------------------------------------------ attend
 
@@ -242,6 +251,8 @@ struct CaCtrl {
   uint64_t full[CA_STAGES], empty[CA_STAGES];
   uint64_t qfull, qempty, vraw, drain;
   uint64_t sfull[2], ready[2], corr[2], ofull[2];
+  uint64_t ifull[CA_ITEMS], iempty[CA_ITEMS];
+  CaItem item[CA_ITEMS];
   uint32_t tmem;
   int abort_flag;
   int kissued, vissued, qissued;
@@ -255,15 +266,13 @@ __device__ __forceinline__ float ca_ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void ca_st32(uint32_t taddr, const uint32_t *r) {
+__device__ __forceinline__ void ca_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void ca_wait_st() {
@@ -286,14 +295,55 @@ __device__ __forceinline__ void ca_tma_4d(uint32_t dst, const CUtensorMap *map, 
       : "memory");
 }
 
+// Bounded wait, as mbar_wait, but a round may sleep up to CA_WAIT_NS until the
+// phase completes: the other warps' polling would take issue slots and
+// instruction fetches from the softmax.
+constexpr uint32_t CA_WAIT_NS = 20000, CA_WAIT_ROUNDS = 1u << 16;
+__device__ __forceinline__ bool ca_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                        unsigned *err) {
+  for (uint32_t i = 0; i < CA_WAIT_ROUNDS; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.b32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(CA_WAIT_NS)
+        : "memory");
+    if (done) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  raise_err(err, ERR_TIMEOUT);
+  return false;
+}
+
 // Whole-warp bounded wait: lane 0 polls.
 __device__ __forceinline__ bool ca_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                              unsigned *err) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err);
+  if ((threadIdx.x & 31) == 0) ok = ca_wait(bar, parity, abort_flag, err);
   ok = __shfl_sync(0xffffffffu, ok, 0);
   return ok;
 }
+
+// The next item of a role's warp (whole warp); false at the end or after an
+// abort. Its fields are in registers afterwards and its slot is given back.
+struct CaItems {
+  int at = 0;
+  __device__ __forceinline__ bool next(CaCtrl &c, CaItem &it, unsigned *err) {
+    const int i = at % CA_ITEMS;
+    if (!ca_wait_warp(smem_u32(&c.ifull[i]), (uint32_t)((at / CA_ITEMS) & 1), &c.abort_flag, err))
+      return false;
+    ++at;
+    const int4 *v = reinterpret_cast<const int4 *>(&c.item[i]);
+    reinterpret_cast<int4 *>(&it)[0] = v[0];
+    reinterpret_cast<int4 *>(&it)[1] = v[1];
+    reinterpret_cast<int4 *>(&it)[2] = v[2];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&c.iempty[i]));
+    return it.b > it.a;
+  }
+};
 
 // The pieces of a step's 128 tokens, one lane each: the page of this lane's
 // piece, -1 for a piece past L or a bad page.
@@ -338,6 +388,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     mbar_init(qempty, 1);
     mbar_init(vraw, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < CA_ITEMS; ++i) {
+      mbar_init(smem_u32(&ctl.ifull[i]), 1);
+      mbar_init(smem_u32(&ctl.iempty[i]), CA_READERS);
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(sfull + 8 * s, 1);
       mbar_init(ready + 8 * s, 8);  // 4 softmax and 4 correction warps
@@ -365,82 +419,89 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t ts = tmem + (uint32_t)(s * 128) + ((uint32_t)((warp & 3) * 32) << 16);
     const float c2 = sl2 > 0.f ? sl2 : 1.f;
     uint32_t sph = 0, oph = 0;
-    CaWalk it(p, blockIdx.x);
+    CaItems items;
+    CaItem it;
     bool ok = true;
-    for (bool more = it.next(true); more && ok; more = it.next(false)) {
-      const int n0 = it.steps0();
+    while (ok && items.next(ctl, it, p.err)) {
+      const int n0 = it.n0;
       const int tok = (it.two() ? s * p.TT : 0) + r / p.G;
-      const bool valid = r < p.TT * p.G && tok < it.gi.z;
-      const int lim = valid ? it.lim0 + tok : 0;
+      const bool valid = r < p.TT * p.G && tok < it.ntok;
+      const int lim = valid ? it.lim0 + tok : 0x7fffffff;
       const bool live = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.f;
       bool any = false;
       for (int j = it.a; j < it.b; ++j) {
-        if (!it.active(s, j, n0)) continue;
+        if (!ca_active(s, j, it.a, n0)) continue;
         ok = ca_wait_warp(sfull + 8 * s, sph, abort_flag, p.err);
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();
         if (live) {
-          float v[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tc_ld32_nowait(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
-          tc_wait_ld();
-          if (!(sl2 > 0.f)) {
-#pragma unroll
-            for (int i = 0; i < 128; ++i) v[i] *= sl2;
-          }
           const int nv = lim - j * CA_KT;  // this row's tokens of the tile
-          if (__any_sync(0xffffffffu, nv < CA_KT)) {
+          const bool mask = __any_sync(0xffffffffu, nv < CA_KT);
+          float mt = -INFINITY, off = 0.f, l0 = 0.f, l1 = 0.f;
+          // two passes over the row, 32 columns at a time (the code of all 128
+          // at once does not stay in the instruction cache): the maximum, then
+          // the exponentials, whose bf16 pairs overwrite columns already read
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t u[32];
+            tc_ld32_nowait(ts + 32 * (c & 3), u);
+            tc_wait_ld();
+            float *v = reinterpret_cast<float *>(u);
+            if (!(sl2 > 0.f)) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i >= nv) v[i] = -INFINITY;
-          }
-          float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+              for (int i = 0; i < 32; ++i) v[i] *= sl2;
+            }
+            if (mask) {
+              const int n = nv - 32 * (c & 3);
 #pragma unroll
-          for (int i = 4; i < 128; i += 4) {
-            t0 = fmaxf(t0, v[i]);
-            t1 = fmaxf(t1, v[i + 1]);
-            t2 = fmaxf(t2, v[i + 2]);
-            t3 = fmaxf(t3, v[i + 3]);
-          }
-          const float mt = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-          float f = 1.f;
-          const float mt2 = ceilf(mt * c2);
-          if (mt2 > m + CA_LAZY || m == -INFINITY) {
-            f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
-            m = fmaxf(m, mt2);
-          }
-          if (any) {
-            ctl.sc[s][r] = __float2bfloat16_rn(f);
-            l *= f;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(corr + 8 * s);
-          }
-          const float off = m == -INFINITY ? 0.f : m;
-          uint32_t pk[64];
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+              for (int i = 0; i < 32; ++i)
+                if (i >= n) v[i] = -INFINITY;
+            }
+            if (c < 4) {
+              float t0 = mt, t1 = v[1], t2 = v[2], t3 = v[3];
+              t0 = fmaxf(t0, v[0]);
 #pragma unroll
-          for (int i = 0; i < 128; i += 4) {
-            const float e0 = ca_ex2(fmaf(v[i], c2, -off)), e1 = ca_ex2(fmaf(v[i + 1], c2, -off));
-            const float e2 = ca_ex2(fmaf(v[i + 2], c2, -off));
-            const float e3 = ca_ex2(fmaf(v[i + 3], c2, -off));
-            l0 += e0;
-            l1 += e1;
-            l2 += e2;
-            l3 += e3;
-            pk[i / 2] = pack_bf16x2(e0, e1);
-            pk[i / 2 + 1] = pack_bf16x2(e2, e3);
+              for (int i = 4; i < 32; i += 4) {
+                t0 = fmaxf(t0, v[i]);
+                t1 = fmaxf(t1, v[i + 1]);
+                t2 = fmaxf(t2, v[i + 2]);
+                t3 = fmaxf(t3, v[i + 3]);
+              }
+              mt = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+              if (c == 3) {
+                float f = 1.f;
+                const float mt2 = ceilf(mt * c2);
+                if (mt2 > m + CA_LAZY || m == -INFINITY) {
+                  f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
+                  m = fmaxf(m, mt2);
+                }
+                if (any) {
+                  ctl.sc[s][r] = __float2bfloat16_rn(valid ? f : 1.f);
+                  l *= f;
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(corr + 8 * s);
+                }
+                off = m == -INFINITY ? 0.f : m;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float e0 = ca_ex2(fmaf(v[i], c2, -off));
+                const float e1 = ca_ex2(fmaf(v[i + 1], c2, -off));
+                l0 += e0;
+                l1 += e1;
+                u[i / 2] = pack_bf16x2(e0, e1);
+              }
+              ca_st16(ts + 16 * (c - 4), u);
+            }
           }
-          ca_st32(ts, pk);
-          ca_st32(ts + 32, pk + 32);
-          l += (l0 + l1) + (l2 + l3);
+          l += l0 + l1;
           ca_wait_st();
         } else if (any) {
           ctl.sc[s][r] = __float2bfloat16_rn(1.f);
@@ -467,19 +528,19 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     }
   } else if (warp < 12) {
     // ------------------------------------------------- correction and results
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     const int r = (warp & 3) * 32 + lane;
     const uint32_t to = tmem + 256u + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t cph[2] = {0, 0}, oph[2] = {0, 0};
-    CaWalk it(p, blockIdx.x);
+    CaItems items;
+    CaItem it;
     bool ok = true;
-    for (bool more = it.next(true); more && ok; more = it.next(false)) {
-      const int n0 = it.steps0();
+    while (ok && items.next(ctl, it, p.err)) {
+      const int n0 = it.n0;
       bool any[2] = {false, false};
       for (int j = it.a; j < it.b && ok; ++j) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (!ok || !it.active(s, j, n0)) continue;
+          if (!ok || !ca_active(s, j, it.a, n0)) continue;
           if (any[s]) {
             ok = ca_wait_warp(corr + 8 * s, cph[s], abort_flag, p.err);
             if (!ok) continue;
@@ -488,13 +549,12 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             if (__any_sync(0xffffffffu, f != 1.f)) {
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tc_ld32_nowait(to + s * 128 + 32 * c, o);
-                tc_wait_ld();
+              for (int c = 0; c < 8; ++c) {
+                float o[16];
+                tc_ld16(to + s * 128 + 16 * c, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                ca_st32(to + s * 128 + 32 * c, o);
+                for (int i = 0; i < 16; ++i) o[i] *= f;
+                ca_st16(to + s * 128 + 16 * c, reinterpret_cast<const uint32_t *>(o));
               }
               ca_wait_st();
             }
@@ -521,13 +581,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      const bool whole = it.a == 0 && it.b == it.gi.w;
+      const bool whole = it.whole != 0;
       const int piece = it.a == 0 ? 1 : 0;  // record of a partial result
       const bool two = it.two();
 #pragma unroll 1
       for (int s = 0; s < (two ? 2 : 1); ++s) {
         const int tok = s * p.TT + r / p.G;
-        const bool valid = r < p.TT * p.G && tok < it.gi.z;
+        const bool valid = r < p.TT * p.G && tok < it.ntok;
         if (!__any_sync(0xffffffffu, valid)) continue;
         // weights of the slot's O (two tiles), or of both slots' (one tile)
         float f0 = 0.f, f1 = 0.f, lse = -INFINITY;
@@ -550,7 +610,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         }
         const bool has = two ? (s == 0 ? any[0] : any[1]) : true;
         const bool has1 = !two && any[1];
-        const size_t row = (size_t)(it.gi.y + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
+        const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
         const size_t rec = ((size_t)blockIdx.x * 2 + piece) * 256 + s * 128 + r;
         if (valid) {
           if (!whole) p.rec_lse[rec] = lse;
@@ -559,64 +619,56 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         if (!has) continue;
         const uint32_t ta = to + (two ? s * 128 : 0);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tc_ld32_nowait(ta + 32 * c, o);
-          tc_wait_ld();
+        for (int c = 0; c < 8; ++c) {
+          float o[16];
+          tc_ld16(ta + 16 * c, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            o[i] = f0 > 0.f ? __float_as_uint(__uint_as_float(o[i]) * f0) : 0u;
+          for (int i = 0; i < 16; ++i) o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
           if (has1) {
-            uint32_t o1[32];
-            tc_ld32_nowait(to + 128 + 32 * c, o1);
-            tc_wait_ld();
+            float o1[16];
+            tc_ld16(to + 128 + 16 * c, o1);
             if (f1 > 0.f) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
+              for (int i = 0; i < 16; ++i) o[i] = fmaf(o1[i], f1, o[i]);
             }
           }
           if (!valid) continue;
           if (whole && p.out_bf16) {
             uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D +
-                                                 32 * c);
+                                                 16 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t x[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                x[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]),
-                                   __uint_as_float(o[8 * i + 2 * k + 1]));
-              d[i] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
+            for (int i = 0; i < 2; ++i)
+              d[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                                pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                                pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
           } else {
-            uint4 *d = reinterpret_cast<uint4 *>(
-                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + 32 * c);
+            float4 *d = reinterpret_cast<float4 *>(
+                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + 16 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              d[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 4; ++i)
+              d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12) {
       // -------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t IDESC_S = f16_idesc(128, 128);
-        constexpr uint32_t IDESC_O = f16_idesc(128, 128) | (1u << 16);  // B = V: MN-major
-        CaWalk it(p, blockIdx.x);
-        uint32_t qph = 0, rph[2] = {0, 0};
-        int cnt = 0;  // steps before the current item
-        bool ok = true;
-        for (bool more = it.next(true); more && ok; more = it.next(false)) {
-          const int n0 = it.steps0();
+      constexpr uint32_t IDESC_S = f16_idesc(128, 128);
+      constexpr uint32_t IDESC_O = f16_idesc(128, 128) | (1u << 16);  // B = V: MN-major
+      CaItems items;
+      CaItem it;
+      uint32_t qph = 0, rph = 0;
+      int pos0 = 0;  // ring position of the item's first K tile
+      bool ok = true;
+      while (ok && items.next(ctl, it, p.err)) {
+        if (lane == 0) {
           const bool two = it.two();
           const int stride = two ? 1 : 2;
           auto scores = [&](int s, int j) -> bool {  // S_s = Q_s K_j^T
-            const int pos = 2 * (cnt + j - it.a), st = pos % CA_STAGES;
-            if (!mbar_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err))
+            const int pos = pos0 + 2 * (j - it.a), st = pos % CA_STAGES;
+            if (!ca_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err))
               return false;
             tc_fence_after();
             const uint64_t da = sw128_desc(q_s + (two ? s * CA_TILE : 0));
@@ -627,59 +679,59 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
               tc_mma(tmem + s * 128, da + o, db + o, IDESC_S, k > 0 ? 1u : 0u);
             }
             tc_commit(sfull + 8 * s);
-            if (!two || s == 1) tc_commit(empty0 + 8 * st);  // the tile's last use
-            // the item's last scores free the query tiles
-            if (two ? (s == 1 && j == it.b - 1) : j == it.b - 1) tc_commit(qempty);
+            const bool last_use = !two || s == 1;
+            if (last_use) tc_commit(empty0 + 8 * st);
+            if (last_use && j == it.b - 1) tc_commit(qempty);  // the query tiles' last use
             return true;
           };
-          ok = mbar_wait(qfull, qph, abort_flag, p.err);
-          if (!ok) break;
-          qph ^= 1u;
-          bool began[2] = {false, false};
+          ok = ca_wait(qfull, qph, abort_flag, p.err);
           for (int s = 0; s < 2 && ok; ++s) {
             const int j = two ? it.a : it.a + s;
-            if (j < it.b && it.active(s, j, n0)) ok = scores(s, j);
+            if (j < it.b && ca_active(s, j, it.a, it.n0)) ok = scores(s, j);
           }
           for (int j = it.a; j < it.b && ok; ++j) {
             for (int s = 0; s < 2 && ok; ++s) {
-              if (!it.active(s, j, n0)) continue;
-              ok = mbar_wait(ready + 8 * s, rph[s], abort_flag, p.err);
+              if (!ca_active(s, j, it.a, it.n0)) continue;
+              ok = ca_wait(ready + 8 * s, (rph >> s) & 1u, abort_flag, p.err);
               if (!ok) break;
-              rph[s] ^= 1u;
-              const int pos = 2 * (cnt + j - it.a) + 1, st = pos % CA_STAGES;
-              ok = mbar_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err);
+              rph ^= 1u << s;
+              const int pos = pos0 + 2 * (j - it.a) + 1, st = pos % CA_STAGES;
+              ok = ca_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err);
               if (!ok) break;
               tc_fence_after();
               // V: 64-value halves CA_HALF apart (leading offset), 8-token
               // groups 1024 bytes apart
               const uint64_t db = (sw128_desc(ring + st * CA_TILE) & ~(0x3fffull << 16)) |
                                   ((uint64_t)(CA_HALF >> 4) << 16);
+              const uint32_t began = j > it.a + (two ? 0 : s) ? 1u : 0u;
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 ca_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k,
-                          db + (uint64_t)((k * 2048) >> 4), IDESC_O, began[s] || k > 0 ? 1u : 0u);
-              began[s] = true;
+                          db + (uint64_t)((k * 2048) >> 4), IDESC_O, k > 0 ? 1u : began);
               if (!two || s == 1) tc_commit(empty0 + 8 * st);
               const int jn = j + stride;
-              if (jn < it.b && it.active(s, jn, n0)) ok = scores(s, jn);
+              if (jn < it.b && ca_active(s, jn, it.a, it.n0)) ok = scores(s, jn);
               else tc_commit(ofull + 8 * s);  // the slot's last product
             }
           }
-          cnt += it.b - it.a;
         }
-        if (!ok) {  // gave up: wait for what was issued
-          tc_commit(drain);
-          mbar_wait(drain, 0, abort_flag, p.err, TC_DRAIN_LIMIT, false);
-        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        qph ^= 1u;
+        pos0 += 2 * (it.b - it.a);
+      }
+      if (ctl.abort_flag && lane == 0) {  // gave up: wait for what was issued
+        tc_commit(drain);
+        mbar_wait(drain, 0, abort_flag, p.err, TC_DRAIN_LIMIT, false);
       }
       __syncwarp();
     } else if (warp == 13) {
       // ------------------------------------------------------------ Q and K tiles
-      CaWalk it(p, blockIdx.x);
+      CaItems items;
+      CaItem it;
       uint32_t qph = 0;
       int cnt = 0, nq = 0;
       bool ok = true;
-      for (bool more = it.next(true); more && ok; more = it.next(false)) {
+      while (ok && items.next(ctl, it, p.err)) {
         if (nq > 0) {
           ok = ca_wait_warp(qempty, qph, abort_flag, p.err);
           if (!ok) break;
@@ -691,13 +743,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           for (int s = 0; s < tiles; ++s)
             for (int h = 0; h < 2; ++h)
               tma_load_3d(q_s + s * CA_TILE + h * CA_HALF, &q_map, qfull, h * 64, it.h * p.G,
-                          it.gi.y + s * p.TT);
+                          it.row0 + s * p.TT);
         }
         ++nq;
-        int page = ca_piece_page(p, it.gi.x, it.L, it.a * CA_KT, lane);
+        int page = ca_piece_page(p, it.seq, it.L, it.a * CA_KT, lane);
         for (int j = it.a; j < it.b; ++j, ++cnt) {
           int np = -1;
-          if (j + 1 < it.b) np = ca_piece_page(p, it.gi.x, it.L, (j + 1) * CA_KT, lane);
+          if (j + 1 < it.b) np = ca_piece_page(p, it.seq, it.L, (j + 1) * CA_KT, lane);
           const int pos = 2 * cnt, st = pos % CA_STAGES;
           ok = ca_wait_warp(empty0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1) ^ 1u, abort_flag,
                             p.err);
@@ -721,15 +773,16 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       }
     } else if (warp == 14) {
       // ------------------------------------------------------------------ V tiles
-      CaWalk it(p, blockIdx.x);
+      CaItems items;
+      CaItem it;
       uint32_t vph = 0;
       int cnt = 0;
       bool ok = true;
-      for (bool more = it.next(true); more && ok; more = it.next(false)) {
-        int page = ca_piece_page(p, it.gi.x, it.L, it.a * CA_KT, lane);
+      while (ok && items.next(ctl, it, p.err)) {
+        int page = ca_piece_page(p, it.seq, it.L, it.a * CA_KT, lane);
         for (int j = it.a; j < it.b; ++j, ++cnt) {
           int np = -1;
-          if (j + 1 < it.b) np = ca_piece_page(p, it.gi.x, it.L, (j + 1) * CA_KT, lane);
+          if (j + 1 < it.b) np = ca_piece_page(p, it.seq, it.L, (j + 1) * CA_KT, lane);
           const int pos = 2 * cnt + 1, st = pos % CA_STAGES;
           ok = ca_wait_warp(empty0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1) ^ 1u, abort_flag,
                             p.err);
@@ -768,6 +821,36 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         }
       }
       if (lane == 0) ctl.vissued = cnt;
+    } else {
+      // ------------------------------------------------------- the items, ahead
+      if (lane == 0) {
+        CaWalk w(p, blockIdx.x);
+        bool more = w.next(true);
+        for (int at = 0;; ++at) {
+          const int i = at % CA_ITEMS;
+          if (!ca_wait(smem_u32(&ctl.iempty[i]), (uint32_t)((at / CA_ITEMS) & 1) ^ 1u, abort_flag,
+                         p.err))
+            break;
+          CaItem &it = ctl.item[i];
+          it.a = it.b = 0;
+          if (more) {
+            it.a = w.a;
+            it.b = w.b;
+            it.n0 = w.w == 2 ? (w.lim0 + p.TT - 1 + CA_KT - 1) / CA_KT : -1;
+            it.ntok = w.gi.z;
+            it.h = w.h;
+            it.row0 = w.gi.y;
+            it.lim0 = w.lim0;
+            it.whole = w.a == 0 && w.b == w.gi.w;
+            it.seq = w.gi.x;
+            it.L = w.L;
+          }
+          mbar_arrive(smem_u32(&ctl.ifull[i]));
+          if (!more) break;
+          more = w.next(false);
+        }
+      }
+      __syncwarp();
     }
   }
 
