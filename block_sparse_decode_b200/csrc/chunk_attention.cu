@@ -62,6 +62,11 @@ constexpr uint32_t CA_TILE = 2 * CA_HALF;
 constexpr uint32_t CA_CTL = 3072;
 constexpr size_t CA_SMEM = CA_CTL + 2 * CA_TILE + CA_STAGES * CA_TILE;
 constexpr int CA_PLAN_THREADS = 1024;
+#ifndef CA_POLY
+#define CA_POLY 0
+#endif
+constexpr float CA_P0 = 0x1.ffffe8p-1f, CA_P1 = 0x1.62e0dcp-1f, CA_P2 = 0x1.ec06dap-3f,
+                CA_P3 = 0x1.ca1446p-5f, CA_P4 = 0x1.3997d6p-7f;
 constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sums
 
 struct CaArgs {
@@ -250,7 +255,7 @@ __device__ __forceinline__ bool ca_active(int s, int j, int a, int n0) {
 struct CaCtrl {
   uint64_t full[CA_STAGES], empty[CA_STAGES];
   uint64_t qfull, qempty, vraw, drain;
-  uint64_t sfull[2], ready[2], corr[2], ofull[2];
+  uint64_t sfull[2], ready[2], ready2[2], corr[2], ofull[2];
   uint64_t ifull[CA_ITEMS], iempty[CA_ITEMS];
   CaItem item[CA_ITEMS];
   uint32_t tmem;
@@ -274,6 +279,53 @@ __device__ __forceinline__ void ca_st16(uint32_t taddr, const uint32_t *r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
+}
+// Two fp32 values in one register pair, and their paired operations.
+__device__ __forceinline__ unsigned long long ca_pair(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void ca_unpair(unsigned long long x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ unsigned long long ca_fma2(unsigned long long a, unsigned long long b,
+                                                      unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long ca_add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ca_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x of a pair on the fp32 units, for x <= 16: x = n + f with n the nearest
+// whole number (left in the low bits of x + 1.5 * 2^23) and |f| <= 1/2, 2^f by a
+// polynomial (Remez exchange on [-1/2, 1/2], relative error 2.6e-6), and n added to its
+// exponent. x below -126 gives 2^-126 instead of 0.
+__device__ __forceinline__ void ca_exp2_poly(unsigned long long x, float &e0, float &e1) {
+  float x0, x1;
+  ca_unpair(x, x0, x1);
+  x = ca_pair(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const unsigned long long big = ca_pair(12582912.f, 12582912.f);
+  const unsigned long long nbig = ca_pair(-12582912.f, -12582912.f);
+  const unsigned long long r = ca_add2(x, big);
+  const unsigned long long f = ca_fma2(ca_add2(r, nbig), ca_pair(-1.f, -1.f), x);
+  unsigned long long y = ca_fma2(f, ca_pair(CA_P4, CA_P4), ca_pair(CA_P3, CA_P3));
+  y = ca_fma2(f, y, ca_pair(CA_P2, CA_P2));
+  y = ca_fma2(f, y, ca_pair(CA_P1, CA_P1));
+  y = ca_fma2(f, y, ca_pair(CA_P0, CA_P0));
+  float r0, r1, y0, y1;
+  ca_unpair(r, r0, r1);
+  ca_unpair(y, y0, y1);
+  e0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23));
+  e1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23));
 }
 __device__ __forceinline__ void ca_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -315,6 +367,18 @@ __device__ __forceinline__ bool ca_wait(uint32_t bar, uint32_t parity, volatile 
   *abort_flag = 1;
   raise_err(err, ERR_TIMEOUT);
   return false;
+}
+
+// The same by every lane of a warp.
+__device__ __forceinline__ bool ca_wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                            unsigned *err) {
+  return __all_sync(0xffffffffu, ca_wait(bar, parity, abort_flag, err));
+}
+
+__device__ __forceinline__ bool ca_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 
 // Whole-warp bounded wait: lane 0 polls.
@@ -377,6 +441,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   const uint32_t qfull = smem_u32(&ctl.qfull), qempty = smem_u32(&ctl.qempty);
   const uint32_t vraw = smem_u32(&ctl.vraw), drain = smem_u32(&ctl.drain);
   const uint32_t sfull = smem_u32(&ctl.sfull[0]), ready = smem_u32(&ctl.ready[0]);
+  const uint32_t ready2 = smem_u32(&ctl.ready2[0]);
   const uint32_t corr = smem_u32(&ctl.corr[0]), ofull = smem_u32(&ctl.ofull[0]);
 
   if (threadIdx.x == 0) {
@@ -395,6 +460,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(sfull + 8 * s, 1);
       mbar_init(ready + 8 * s, 8);  // 4 softmax and 4 correction warps
+      mbar_init(ready2 + 8 * s, 4);
       mbar_init(corr + 8 * s, 4);
       mbar_init(ofull + 8 * s, 1);
     }
@@ -412,13 +478,14 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they start at 0
   volatile int *abort_flag = &ctl.abort_flag;
   const float sl2 = p.scale * 1.4426950408889634f;
   pdl_wait();
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t ts = tmem + (uint32_t)(s * 128) + ((uint32_t)((warp & 3) * 32) << 16);
     const float c2 = sl2 > 0.f ? sl2 : 1.f;
@@ -436,82 +503,136 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       bool any = false;
       for (int j = it.a; j < it.b; ++j) {
         if (!ca_active(s, j, it.a, n0)) continue;
-        ok = ca_wait_warp(sfull + 8 * s, sph, abort_flag, p.err);
+        ok = ca_wait_all(sfull + 8 * s, sph, abort_flag, p.err);
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();
         if (live) {
           const int nv = lim - j * CA_KT;  // this row's tokens of the tile
-          const bool mask = __any_sync(0xffffffffu, nv < CA_KT);
-          float mt = -INFINITY, off = 0.f, l0 = 0.f, l1 = 0.f;
-          // two passes over the row, 32 columns at a time (the code of all 128
-          // at once does not stay in the instruction cache): the maximum, then
-          // the exponentials, whose bf16 pairs overwrite columns already read
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t u[32];
-            tc_ld32_nowait(ts + 32 * (c & 3), u);
-            tc_wait_ld();
+          const bool mask = __any_sync(0xffffffffu, nv < CA_KT) || !(sl2 > 0.f);
+          // the row's new maximum, its rescaling for the correction warps, and
+          // what the exponentials subtract
+          auto grow = [&](float mt) {
+            float f = 1.f;
+            const float mt2 = ceilf(mt * c2);
+            if (mt2 > m + CA_LAZY || m == -INFINITY) {
+              f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
+              m = fmaxf(m, mt2);
+            }
+            if (any) {
+              ctl.sc[s][r] = __float2bfloat16_rn(valid ? f : 1.f);
+              l *= f;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(corr + 8 * s);
+            }
+            return m == -INFINITY ? 0.f : m;
+          };
+          // the first 64 columns of P are written: their product may begin
+          auto half_ready = [&]() {
+            ca_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready + 8 * s);
+          };
+          float l0 = 0.f, l1 = 0.f;
+          if (!mask) {
+            uint32_t u[128];
             float *v = reinterpret_cast<float *>(u);
-            if (!(sl2 > 0.f)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= sl2;
+            for (int c = 0; c < 4; ++c)
+              tc_ld32_nowait(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(u + 32 * c));
+            tc_wait_ld();
+            float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+#pragma unroll
+            for (int i = 4; i < 124; i += 8) {
+              t0 = ca_max3(t0, v[i], v[i + 1]);
+              t1 = ca_max3(t1, v[i + 2], v[i + 3]);
+              t2 = ca_max3(t2, v[i + 4], v[i + 5]);
+              t3 = ca_max3(t3, v[i + 6], v[i + 7]);
             }
-            if (mask) {
+            t0 = ca_max3(t0, v[124], v[125]);
+            t1 = ca_max3(t1, v[126], v[127]);
+            const float off = grow(ca_max3(fmaxf(t0, t1), t2, t3));
+            const unsigned long long cc = ca_pair(c2, c2), oo = ca_pair(-off, -off);
+            unsigned long long la = ca_pair(0.f, 0.f), lb = la;
+            // the exponentials in a loop over 32 columns, read again (unrolled
+            // over the row they do not stay in the instruction cache); the next
+            // columns are on their way meanwhile
+            tc_ld32_nowait(ts, *reinterpret_cast<uint32_t(*)[32]>(u));
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tc_wait_ld();
+              unsigned long long x[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                x[i] = ca_fma2(ca_pair(v[2 * i], v[2 * i + 1]), cc, oo);
+              if (c < 3) tc_ld32_nowait(ts + 32 * (c + 1), *reinterpret_cast<uint32_t(*)[32]>(u));
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float e0, e1;
+                if (i % 8 < CA_POLY / 2) {
+                  ca_exp2_poly(x[i], e0, e1);
+                } else {
+                  ca_unpair(x[i], e0, e1);
+                  e0 = ca_ex2(e0);
+                  e1 = ca_ex2(e1);
+                }
+                if (i % 2 == 0) la = ca_add2(la, ca_pair(e0, e1));
+                else lb = ca_add2(lb, ca_pair(e0, e1));
+                pk[i] = pack_bf16x2(e0, e1);
+              }
+              ca_st16(ts + 16 * c, pk);
+              if (c == 1) half_ready();
+            }
+            float a0, a1, b0, b1;
+            ca_unpair(la, a0, a1);
+            ca_unpair(lb, b0, b1);
+            l0 = a0 + b0;
+            l1 = a1 + b1;
+          } else {
+            // a tile with masked columns (or a scale that is not positive): two
+            // passes of 32 columns at a time
+            float mt = -INFINITY, off = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t u[32];
+              tc_ld32_nowait(ts + 32 * (c & 3), u);
+              tc_wait_ld();
+              float *v = reinterpret_cast<float *>(u);
               const int n = nv - 32 * (c & 3);
+              const float pre = sl2 > 0.f ? 1.f : sl2;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i >= n) v[i] = -INFINITY;
-            }
-            if (c < 4) {
-              float t0 = mt, t1 = v[1], t2 = v[2], t3 = v[3];
-              t0 = fmaxf(t0, v[0]);
+              for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] * pre : -INFINITY;
+              if (c < 4) {
 #pragma unroll
-              for (int i = 4; i < 32; i += 4) {
-                t0 = fmaxf(t0, v[i]);
-                t1 = fmaxf(t1, v[i + 1]);
-                t2 = fmaxf(t2, v[i + 2]);
-                t3 = fmaxf(t3, v[i + 3]);
-              }
-              mt = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-              if (c == 3) {
-                float f = 1.f;
-                const float mt2 = ceilf(mt * c2);
-                if (mt2 > m + CA_LAZY || m == -INFINITY) {
-                  f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
-                  m = fmaxf(m, mt2);
+                for (int i = 0; i < 32; ++i) mt = fmaxf(mt, v[i]);
+                if (c == 3) off = grow(mt);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const float e0 = ca_ex2(fmaf(v[i], c2, -off));
+                  const float e1 = ca_ex2(fmaf(v[i + 1], c2, -off));
+                  l0 += e0;
+                  l1 += e1;
+                  u[i / 2] = pack_bf16x2(e0, e1);
                 }
-                if (any) {
-                  ctl.sc[s][r] = __float2bfloat16_rn(valid ? f : 1.f);
-                  l *= f;
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(corr + 8 * s);
-                }
-                off = m == -INFINITY ? 0.f : m;
+                ca_st16(ts + 16 * (c - 4), u);
+                if (c == 5) half_ready();
               }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float e0 = ca_ex2(fmaf(v[i], c2, -off));
-                const float e1 = ca_ex2(fmaf(v[i + 1], c2, -off));
-                l0 += e0;
-                l1 += e1;
-                u[i / 2] = pack_bf16x2(e0, e1);
-              }
-              ca_st16(ts + 16 * (c - 4), u);
             }
           }
           l += l0 + l1;
           ca_wait_st();
-        } else if (any) {
-          ctl.sc[s][r] = __float2bfloat16_rn(1.f);
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(corr + 8 * s);
+          if (lane == 0) mbar_arrive(ready2 + 8 * s);
+        } else if (lane == 0) {  // no rows here: P may hold anything
+          if (any) mbar_arrive(corr + 8 * s);
+          mbar_arrive(ready + 8 * s);
+          mbar_arrive(ready2 + 8 * s);
         }
         any = true;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ready + 8 * s);
       }
       if (!ok) break;
       if (any) {  // the item's maximum and sum, for its end
@@ -528,6 +649,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     }
   } else if (warp < 12) {
     // ------------------------------------------------- correction and results
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     const int r = (warp & 3) * 32 + lane;
     const uint32_t to = tmem + 256u + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t cph[2] = {0, 0}, oph[2] = {0, 0};
@@ -537,6 +659,11 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     while (ok && items.next(ctl, it, p.err)) {
       const int n0 = it.n0;
       bool any[2] = {false, false};
+      bool live[2];  // whether the softmax warp of these rows has any of the item's
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        live[s] = __any_sync(0xffffffffu, r < p.TT * p.G &&
+                                              (it.two() ? s * p.TT : 0) + r / p.G < it.ntok);
       for (int j = it.a; j < it.b && ok; ++j) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -545,7 +672,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             ok = ca_wait_warp(corr + 8 * s, cph[s], abort_flag, p.err);
             if (!ok) continue;
             cph[s] ^= 1u;
-            const float f = __bfloat162float(ctl.sc[s][r]);
+            const float f = live[s] ? __bfloat162float(ctl.sc[s][r]) : 1.f;
             if (__any_sync(0xffffffffu, f != 1.f)) {
               tc_fence_after();
 #pragma unroll 1
@@ -653,6 +780,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       }
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 12) {
       // -------------------------------------------------------------- MMA issuer
       constexpr uint32_t IDESC_S = f16_idesc(128, 128);
@@ -662,64 +790,92 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       uint32_t qph = 0, rph = 0;
       int pos0 = 0;  // ring position of the item's first K tile
       bool ok = true;
+      // the whole warp runs this loop, so that the operands of the MMAs are
+      // warp-uniform; one elected lane issues them
+      const bool lead = ca_elect();
       while (ok && items.next(ctl, it, p.err)) {
-        if (lane == 0) {
-          const bool two = it.two();
-          const int stride = two ? 1 : 2;
-          auto scores = [&](int s, int j) -> bool {  // S_s = Q_s K_j^T
-            const int pos = pos0 + 2 * (j - it.a), st = pos % CA_STAGES;
-            if (!ca_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err))
-              return false;
-            tc_fence_after();
-            const uint64_t da = sw128_desc(q_s + (two ? s * CA_TILE : 0));
-            const uint64_t db = sw128_desc(ring + st * CA_TILE);
+        const bool two = it.two();
+        const int a = it.a, b = it.b, n0 = it.n0, stride = two ? 1 : 2;
+        auto tile_in = [&](int pos) {  // a tile of the ring has landed
+          return ca_wait_all(full0 + 8 * (pos % CA_STAGES), (uint32_t)((pos / CA_STAGES) & 1),
+                             abort_flag, p.err);
+        };
+        auto scores = [&](int s, int j) {  // S_s = Q_s K_j^T, by the elected lane
+          const int st = (pos0 + 2 * (j - a)) % CA_STAGES;
+          const uint64_t da = sw128_desc(q_s + (two ? s * CA_TILE : 0));
+          const uint64_t db = sw128_desc(ring + st * CA_TILE);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint64_t o = (uint64_t)(((k >> 2) * CA_HALF + (k & 3) * 32) >> 4);
-              tc_mma(tmem + s * 128, da + o, db + o, IDESC_S, k > 0 ? 1u : 0u);
-            }
-            tc_commit(sfull + 8 * s);
-            const bool last_use = !two || s == 1;
-            if (last_use) tc_commit(empty0 + 8 * st);
-            if (last_use && j == it.b - 1) tc_commit(qempty);  // the query tiles' last use
-            return true;
-          };
-          ok = ca_wait(qfull, qph, abort_flag, p.err);
-          for (int s = 0; s < 2 && ok; ++s) {
-            const int j = two ? it.a : it.a + s;
-            if (j < it.b && ca_active(s, j, it.a, it.n0)) ok = scores(s, j);
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t o = (uint64_t)(((k >> 2) * CA_HALF + (k & 3) * 32) >> 4);
+            tc_mma(s * 128, da + o, db + o, IDESC_S, k > 0 ? 1u : 0u);
           }
-          for (int j = it.a; j < it.b && ok; ++j) {
-            for (int s = 0; s < 2 && ok; ++s) {
-              if (!ca_active(s, j, it.a, it.n0)) continue;
-              ok = ca_wait(ready + 8 * s, (rph >> s) & 1u, abort_flag, p.err);
-              if (!ok) break;
-              rph ^= 1u << s;
-              const int pos = pos0 + 2 * (j - it.a) + 1, st = pos % CA_STAGES;
-              ok = ca_wait(full0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1), abort_flag, p.err);
-              if (!ok) break;
-              tc_fence_after();
-              // V: 64-value halves CA_HALF apart (leading offset), 8-token
-              // groups 1024 bytes apart
-              const uint64_t db = (sw128_desc(ring + st * CA_TILE) & ~(0x3fffull << 16)) |
-                                  ((uint64_t)(CA_HALF >> 4) << 16);
-              const uint32_t began = j > it.a + (two ? 0 : s) ? 1u : 0u;
+          tc_commit(sfull + 8 * s);
+          if (!two || s == 1) {  // the tile's last use, and the query tiles'
+            tc_commit(empty0 + 8 * st);
+            if (j == b - 1) tc_commit(qempty);
+          }
+        };
+        ok = ca_wait_all(qfull, qph, abort_flag, p.err);
+        for (int s = 0; s < 2 && ok; ++s) {
+          const int j = two ? a : a + s;
+          if (j >= b || !ca_active(s, j, a, n0)) continue;
+          ok = tile_in(pos0 + 2 * (j - a));
+          tc_fence_after();
+          if (ok && lead) scores(s, j);
+          __syncwarp();
+        }
+        // a wait costs about 120 clocks even when there is nothing to wait for:
+        // the tiles are waited for before P, which arrives last
+        int kin = a + stride - 1, vin = a - 1;  // last steps whose K, V tiles are in
+        for (int j = a; j < b && ok; ++j) {
+          for (int s = 0; s < 2; ++s) {
+            if (!ca_active(s, j, a, n0)) continue;
+            const int jn = j + stride;
+            const bool more = jn < b && ca_active(s, jn, a, n0);
+            if (vin < j) {
+              ok = tile_in(pos0 + 2 * (j - a) + 1);
+              vin = j;
+            }
+            if (ok && more && kin < jn) {
+              ok = tile_in(pos0 + 2 * (jn - a));
+              kin = jn;
+            }
+            const uint32_t ph = (rph >> s) & 1u;
+            ok = ok && ca_wait_all(ready + 8 * s, ph, abort_flag, p.err);
+            if (!ok) break;
+            rph ^= 1u << s;
+            tc_fence_after();
+            const int st = (pos0 + 2 * (j - a) + 1) % CA_STAGES;
+            // V: 64-value halves CA_HALF apart (leading offset), 8-token
+            // groups 1024 bytes apart
+            const uint64_t db = (sw128_desc(ring + st * CA_TILE) & ~(0x3fffull << 16)) |
+                                ((uint64_t)(CA_HALF >> 4) << 16);
+            if (lead) {
+              const uint32_t began = j > a + (two ? 0 : s) ? 1u : 0u;
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                ca_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k,
-                          db + (uint64_t)((k * 2048) >> 4), IDESC_O, k > 0 ? 1u : began);
+              for (int k = 0; k < 4; ++k)
+                ca_mma_ts(256 + s * 128, s * 128 + 8 * k, db + (uint64_t)((k * 2048) >> 4), IDESC_O,
+                          k > 0 ? 1u : began);
+            }
+            ok = ca_wait_all(ready2 + 8 * s, ph, abort_flag, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+              for (int k = 4; k < 8; ++k)
+                ca_mma_ts(256 + s * 128, s * 128 + 8 * k, db + (uint64_t)((k * 2048) >> 4), IDESC_O,
+                          1u);
               if (!two || s == 1) tc_commit(empty0 + 8 * st);
-              const int jn = j + stride;
-              if (jn < it.b && ca_active(s, jn, it.a, it.n0)) ok = scores(s, jn);
+              if (more) scores(s, jn);
               else tc_commit(ofull + 8 * s);  // the slot's last product
             }
+            __syncwarp();
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         qph ^= 1u;
         pos0 += 2 * (it.b - it.a);
       }
-      if (ctl.abort_flag && lane == 0) {  // gave up: wait for what was issued
+      if (ctl.abort_flag && lead) {  // gave up: wait for what was issued
         tc_commit(drain);
         mbar_wait(drain, 0, abort_flag, p.err, TC_DRAIN_LIMIT, false);
       }
