@@ -79,6 +79,7 @@ struct CaArgs {
   void *out;
   float *lse;
   int S, Nq, Gmax, Hq, Hkv, G, TT, P, box, max_pages, num_pages, out_bf16;
+  int tile_pages, tile_slots;  // a step's 128 tokens in whole pages and slots
   float scale;
   unsigned *err;
 };
@@ -375,6 +376,22 @@ __device__ __forceinline__ bool ca_wait_all(uint32_t bar, uint32_t parity, volat
   return __all_sync(0xffffffffu, ca_wait(bar, parity, abort_flag, err));
 }
 
+// Both of two barriers, whose checks overlap.
+__device__ __forceinline__ bool ca_wait_all2(uint32_t bar, uint32_t parity, uint32_t bar2,
+                                             uint32_t parity2, volatile int *abort_flag,
+                                             unsigned *err) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n"
+      " selp.b32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(bar2), "r"(parity2)
+      : "memory");
+  if (__all_sync(0xffffffffu, done)) return true;
+  return ca_wait_all(bar, parity, abort_flag, err) && ca_wait_all(bar2, parity2, abort_flag, err);
+}
+
 __device__ __forceinline__ bool ca_elect() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
@@ -409,17 +426,70 @@ struct CaItems {
   }
 };
 
-// The pieces of a step's 128 tokens, one lane each: the page of this lane's
-// piece, -1 for a piece past L or a bad page.
-__device__ __forceinline__ int ca_piece_page(const CaArgs &p, int s, int L, int tok0, int lane) {
-  const int t = tok0 + lane * p.box;
-  if (lane * p.box >= CA_KT || t >= L) return -1;
-  const int page = __ldg(p.block_table + (size_t)s * p.max_pages + t / p.P);
-  if (page < 0 || page >= p.num_pages) {
-    raise_err(p.err, ERR_PAGE);
-    return -1;
+// The pieces of the steps' 128 tokens, one lane each, in step order: where
+// they lie in their pages, and the page ids, read two steps ahead. (A piece of
+// `box` tokens never crosses a page. No division per step: the loaders' few
+// instructions are on the path from a free stage to its next tile.)
+struct CaPieces {
+  static constexpr int NONE = -0x7fffffff - 1;
+  const int32_t *row;  // the sequence's block-table row, at the page read next
+  int tok, rslot, L;   // the piece read next: its first token, its slot
+  int slot;            // the slot of the step being issued
+  int id[2];
+  __device__ __forceinline__ void start(const CaArgs &p, const CaItem &it, int lane) {
+    const bool has = lane * p.box < CA_KT;
+    tok = it.a * CA_KT + (has ? lane * p.box : 0);
+    L = has ? it.L : 0;
+    const int col = tok / p.P;
+    slot = rslot = tok - col * p.P;
+    row = p.block_table + (size_t)it.seq * p.max_pages + col;
+    id[0] = read(p);
+    id[1] = read(p);
   }
-  return page;
+  __device__ __forceinline__ int read(const CaArgs &p) {
+    if (tok >= L) return NONE;
+    const int v = __ldg(row);
+    tok += CA_KT;
+    rslot += p.tile_slots;
+    row += p.tile_pages;
+    if (rslot >= p.P) {
+      rslot -= p.P;
+      ++row;
+    }
+    return v;
+  }
+  // The page of this step's piece (-1: past L, or a bad page).
+  __device__ __forceinline__ int take(const CaArgs &p) {
+    int v = id[0];
+    id[0] = id[1];
+    id[1] = read(p);
+    if (v < 0 || v >= p.num_pages) {
+      if (v != NONE) raise_err(p.err, ERR_PAGE);
+      v = -1;
+    }
+    return v;
+  }
+  __device__ __forceinline__ void step(const CaArgs &p) {
+    slot += p.tile_slots;
+    if (slot >= p.P) slot -= p.P;
+  }
+};
+
+// Issues a step's tile: every piece's two halves of 64 values, by the elected
+// lane. `slot` is this lane's piece's slot in its page. Returns the bytes.
+__device__ __forceinline__ void ca_load_tile(const CaArgs &p, const CUtensorMap *map, uint32_t dst,
+                                             uint32_t bar, int page, int slot, int h, bool lead) {
+  const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+  if (lead) mbar_arrive_expect(bar, (uint32_t)(__popc(live) * p.box * 256));
+  __syncwarp();
+  for (int i = 0, off = 0; off < CA_KT; ++i, off += p.box) {
+    const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, slot, i);
+    if (pg >= 0 && lead) {
+      ca_tma_4d(dst + off * 128, map, bar, 0, h, sl, pg);
+      ca_tma_4d(dst + CA_HALF + off * 128, map, bar, 64, h, sl, pg);
+    }
+  }
+  __syncwarp();
 }
 
 __global__ void __launch_bounds__(CA_THREADS, 1)
@@ -568,19 +638,23 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
                 x[i] = ca_fma2(ca_pair(v[2 * i], v[2 * i + 1]), cc, oo);
               if (c < 3) tc_ld32_nowait(ts + 32 * (c + 1), *reinterpret_cast<uint32_t(*)[32]>(u));
               uint32_t pk[16];
+              float e[32];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                float e0, e1;
                 if (i % 8 < CA_POLY / 2) {
-                  ca_exp2_poly(x[i], e0, e1);
+                  ca_exp2_poly(x[i], e[2 * i], e[2 * i + 1]);
                 } else {
-                  ca_unpair(x[i], e0, e1);
-                  e0 = ca_ex2(e0);
-                  e1 = ca_ex2(e1);
+                  ca_unpair(x[i], e[2 * i], e[2 * i + 1]);
+                  e[2 * i] = ca_ex2(e[2 * i]);
+                  e[2 * i + 1] = ca_ex2(e[2 * i + 1]);
                 }
-                if (i % 2 == 0) la = ca_add2(la, ca_pair(e0, e1));
-                else lb = ca_add2(lb, ca_pair(e0, e1));
-                pk[i] = pack_bf16x2(e0, e1);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                la = ca_add2(la, ca_pair(e[2 * i], e[2 * i + 1]));
+                lb = ca_add2(lb, ca_pair(e[2 * i + 2], e[2 * i + 3]));
               }
               ca_st16(ts + 16 * c, pk);
               if (c == 1) half_ready();
@@ -788,7 +862,12 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       CaItems items;
       CaItem it;
       uint32_t qph = 0, rph = 0;
-      int pos0 = 0;  // ring position of the item's first K tile
+      int kst = 0, vst = 1;  // the stages of the next K and V tile, and their phases
+      uint32_t kph = 0, vph = 0;
+      // V: 64-value halves CA_HALF apart (leading offset), 8-token groups 1024
+      // bytes apart
+      const uint64_t q_desc = sw128_desc(q_s), k_desc = sw128_desc(ring);
+      const uint64_t v_desc = (k_desc & ~(0x3fffull << 16)) | ((uint64_t)(CA_HALF >> 4) << 16);
       bool ok = true;
       // the whole warp runs this loop, so that the operands of the MMAs are
       // warp-uniform; one elected lane issues them
@@ -796,60 +875,56 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       while (ok && items.next(ctl, it, p.err)) {
         const bool two = it.two();
         const int a = it.a, b = it.b, n0 = it.n0, stride = two ? 1 : 2;
-        auto tile_in = [&](int pos) {  // a tile of the ring has landed
-          return ca_wait_all(full0 + 8 * (pos % CA_STAGES), (uint32_t)((pos / CA_STAGES) & 1),
-                             abort_flag, p.err);
-        };
-        auto scores = [&](int s, int j) {  // S_s = Q_s K_j^T, by the elected lane
-          const int st = (pos0 + 2 * (j - a)) % CA_STAGES;
-          const uint64_t da = sw128_desc(q_s + (two ? s * CA_TILE : 0));
-          const uint64_t db = sw128_desc(ring + st * CA_TILE);
+        // S_s = Q_s K^T with the K tile at the ring's next even position, by
+        // the elected lane
+        auto scores = [&](int s, bool last_use, bool last) {
+          const uint64_t da = q_desc + (uint64_t)(two ? s * (CA_TILE >> 4) : 0);
+          const uint64_t db = k_desc + (uint64_t)(kst * (CA_TILE >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t o = (uint64_t)(((k >> 2) * CA_HALF + (k & 3) * 32) >> 4);
             tc_mma(s * 128, da + o, db + o, IDESC_S, k > 0 ? 1u : 0u);
           }
           tc_commit(sfull + 8 * s);
-          if (!two || s == 1) {  // the tile's last use, and the query tiles'
-            tc_commit(empty0 + 8 * st);
-            if (j == b - 1) tc_commit(qempty);
+          if (last_use) {
+            tc_commit(empty0 + 8 * kst);
+            if (last) tc_commit(qempty);  // the query tiles' last use
+          }
+        };
+        auto next_k = [&]() {
+          kst += 2;
+          if (kst >= CA_STAGES) {
+            kst -= CA_STAGES;
+            kph ^= 1u;
           }
         };
         ok = ca_wait_all(qfull, qph, abort_flag, p.err);
-        for (int s = 0; s < 2 && ok; ++s) {
-          const int j = two ? a : a + s;
-          if (j >= b || !ca_active(s, j, a, n0)) continue;
-          ok = tile_in(pos0 + 2 * (j - a));
+        for (int i = 0; i < (two ? 1 : 2) && ok && a + i < b; ++i) {
+          ok = ca_wait_all(full0 + 8 * kst, kph, abort_flag, p.err);
           tc_fence_after();
-          if (ok && lead) scores(s, j);
+          if (ok && lead) {
+            const bool last = a + i == b - 1;
+            if (two && a < n0) scores(0, false, false);
+            scores(two ? 1 : i, true, last);
+          }
           __syncwarp();
+          next_k();
         }
-        // a wait costs about 120 clocks even when there is nothing to wait for:
-        // the tiles are waited for before P, which arrives last
-        int kin = a + stride - 1, vin = a - 1;  // last steps whose K, V tiles are in
+        // few instructions between the waits, and the tiles' waits ahead of
+        // P's, which arrives last: this warp's latency is on every slot's path
         for (int j = a; j < b && ok; ++j) {
-          for (int s = 0; s < 2; ++s) {
-            if (!ca_active(s, j, a, n0)) continue;
-            const int jn = j + stride;
-            const bool more = jn < b && ca_active(s, jn, a, n0);
-            if (vin < j) {
-              ok = tile_in(pos0 + 2 * (j - a) + 1);
-              vin = j;
-            }
-            if (ok && more && kin < jn) {
-              ok = tile_in(pos0 + 2 * (jn - a));
-              kin = jn;
-            }
+          const int jn = j + stride;
+          const int s0 = two ? (j < n0 ? 0 : 1) : ((j - a) & 1), s1 = two ? 1 : s0;
+          ok = ca_wait_all2(full0 + 8 * vst, vph, full0 + 8 * (jn < b ? kst : vst),
+                            jn < b ? kph : vph, abort_flag, p.err);
+#pragma unroll 1
+          for (int s = s0; s <= s1 && ok; ++s) {
             const uint32_t ph = (rph >> s) & 1u;
-            ok = ok && ca_wait_all(ready + 8 * s, ph, abort_flag, p.err);
+            ok = ca_wait_all(ready + 8 * s, ph, abort_flag, p.err);
             if (!ok) break;
             rph ^= 1u << s;
             tc_fence_after();
-            const int st = (pos0 + 2 * (j - a) + 1) % CA_STAGES;
-            // V: 64-value halves CA_HALF apart (leading offset), 8-token
-            // groups 1024 bytes apart
-            const uint64_t db = (sw128_desc(ring + st * CA_TILE) & ~(0x3fffull << 16)) |
-                                ((uint64_t)(CA_HALF >> 4) << 16);
+            const uint64_t db = v_desc + (uint64_t)(vst * (CA_TILE >> 4));
             if (lead) {
               const uint32_t began = j > a + (two ? 0 : s) ? 1u : 0u;
 #pragma unroll
@@ -865,15 +940,20 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
               for (int k = 4; k < 8; ++k)
                 ca_mma_ts(256 + s * 128, s * 128 + 8 * k, db + (uint64_t)((k * 2048) >> 4), IDESC_O,
                           1u);
-              if (!two || s == 1) tc_commit(empty0 + 8 * st);
-              if (more) scores(s, jn);
+              if (s == s1) tc_commit(empty0 + 8 * vst);
+              if (jn < b && (!two || s == 1 || jn < n0)) scores(s, s == s1, jn == b - 1);
               else tc_commit(ofull + 8 * s);  // the slot's last product
             }
             __syncwarp();
           }
+          if (jn < b) next_k();
+          vst += 2;
+          if (vst >= CA_STAGES) {
+            vst -= CA_STAGES;
+            vph ^= 1u;
+          }
         }
         qph ^= 1u;
-        pos0 += 2 * (it.b - it.a);
       }
       if (ctl.abort_flag && lead) {  // gave up: wait for what was issued
         tc_commit(drain);
@@ -884,8 +964,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       // ------------------------------------------------------------ Q and K tiles
       CaItems items;
       CaItem it;
-      uint32_t qph = 0;
-      int cnt = 0, nq = 0;
+      CaPieces pieces;
+      const bool lead = ca_elect();
+      uint32_t qph = 0, ph = 0;
+      int cnt = 0, nq = 0, st = 0;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
         if (nq > 0) {
@@ -893,7 +975,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           if (!ok) break;
           qph ^= 1u;
         }
-        if (lane == 0) {
+        if (lead) {
           const int tiles = it.two() ? 2 : 1;
           mbar_arrive_expect(qfull, (uint32_t)(tiles * 2 * p.TT * p.G * 128));
           for (int s = 0; s < tiles; ++s)
@@ -902,25 +984,19 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
                           it.row0 + s * p.TT);
         }
         ++nq;
-        int page = ca_piece_page(p, it.seq, it.L, it.a * CA_KT, lane);
+        pieces.start(p, it, lane);
         for (int j = it.a; j < it.b; ++j, ++cnt) {
-          int np = -1;
-          if (j + 1 < it.b) np = ca_piece_page(p, it.seq, it.L, (j + 1) * CA_KT, lane);
-          const int pos = 2 * cnt, st = pos % CA_STAGES;
-          ok = ca_wait_warp(empty0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1) ^ 1u, abort_flag,
-                            p.err);
+          const int page = pieces.take(p);
+          ok = ca_wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
           if (!ok) break;
-          const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
-          const uint32_t dst = ring + st * CA_TILE, bar = full0 + 8 * st;
-          if (lane == 0) mbar_arrive_expect(bar, (uint32_t)(__popc(live) * p.box * 256));
-          __syncwarp();
-          if (page >= 0) {
-            const int slot = (j * CA_KT + lane * p.box) % p.P;
-            for (int h = 0; h < 2; ++h)
-              ca_tma_4d(dst + h * CA_HALF + lane * p.box * 128, &k_map, bar, h * 64, it.h, slot,
-                        page);
+          ca_load_tile(p, &k_map, ring + st * CA_TILE, full0 + 8 * st, page, pieces.slot, it.h,
+                       lead);
+          pieces.step(p);
+          st += 2;  // K tiles are the ring's even positions
+          if (st >= CA_STAGES) {
+            st -= CA_STAGES;
+            ph ^= 1u;
           }
-          page = np;
         }
       }
       if (lane == 0) {
@@ -931,30 +1007,22 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       // ------------------------------------------------------------------ V tiles
       CaItems items;
       CaItem it;
-      uint32_t vph = 0;
-      int cnt = 0;
+      CaPieces pieces;
+      const bool lead = ca_elect();
+      uint32_t vph = 0, ph = 0;
+      int cnt = 0, st = 1;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
-        int page = ca_piece_page(p, it.seq, it.L, it.a * CA_KT, lane);
+        pieces.start(p, it, lane);
         for (int j = it.a; j < it.b; ++j, ++cnt) {
-          int np = -1;
-          if (j + 1 < it.b) np = ca_piece_page(p, it.seq, it.L, (j + 1) * CA_KT, lane);
-          const int pos = 2 * cnt + 1, st = pos % CA_STAGES;
-          ok = ca_wait_warp(empty0 + 8 * st, (uint32_t)((pos / CA_STAGES) & 1) ^ 1u, abort_flag,
-                            p.err);
+          const int page = pieces.take(p);
+          ok = ca_wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
           if (!ok) break;
           const int nrow = it.L - j * CA_KT;  // the tile's rows that hold tokens
           const bool tail = nrow < CA_KT;
-          const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
-          const uint32_t dst = ring + st * CA_TILE, bar = tail ? vraw : full0 + 8 * st;
-          if (lane == 0) mbar_arrive_expect(bar, (uint32_t)(__popc(live) * p.box * 256));
-          __syncwarp();
-          if (page >= 0) {
-            const int slot = (j * CA_KT + lane * p.box) % p.P;
-            for (int h = 0; h < 2; ++h)
-              ca_tma_4d(dst + h * CA_HALF + lane * p.box * 128, &v_map, bar, h * 64, it.h, slot,
-                        page);
-          }
+          const uint32_t dst = ring + st * CA_TILE;
+          ca_load_tile(p, &v_map, dst, tail ? vraw : full0 + 8 * st, page, pieces.slot, it.h, lead);
+          pieces.step(p);
           if (tail) {
             // (its own copies: waited for even after another role gave up)
             bool in = true;
@@ -973,7 +1041,11 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(full0 + 8 * st);
           }
-          page = np;
+          st += 2;  // V tiles are the odd positions
+          if (st >= CA_STAGES) {
+            st -= CA_STAGES;
+            ph ^= 1u;
+          }
         }
       }
       if (lane == 0) ctl.vissued = cnt;
@@ -1159,6 +1231,8 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   a.TT = l.TT;
   a.P = d.P;
   a.box = std::min(d.P & -d.P, CA_KT);  // a piece never crosses a page
+  a.tile_pages = CA_KT / d.P;
+  a.tile_slots = CA_KT % d.P;
   a.max_pages = c.max_pages_per_seq;
   a.num_pages = c.num_pages;
   a.out_bf16 = out_is_bf16;
