@@ -22,14 +22,14 @@
 // step and slot S = Q K^T (M = N = K = 128), the softmax of S as bf16 P in
 // tensor memory over S itself, and O += P V, both tcgen05. While one slot's
 // warps work on its softmax, the tensor cores work for the other.
-//   warps 0-3, 4-7  softmax of slot 0, 1: a thread holds a row of S, so the
-//                   row's maximum and sum need no exchange
-//   warps 8-11      rescale O where a maximum grew; at an item's end read O
+//   warps 0-7, 8-15 softmax of slot 0, 1: a thread holds half a row of S (two
+//                   warps hold a row's halves, and exchange its maximum)
+//   warps 16-19     rescale O where a maximum grew; at an item's end read O
 //                   and write the result
-//   warp 12         issues the MMAs
-//   warp 13, 14     TMA of Q and K tiles; of V tiles, whose rows past L_s are
+//   warp 20         issues the MMAs
+//   warp 21, 22     TMA of Q and K tiles; of V tiles, whose rows past L_s are
 //                   set to zero (0 * NaN in a stale slot would reach the sum)
-//   warp 15         announces the items to the other warps, a few ahead
+//   warp 23         announces the items to the other warps, a few ahead
 // The maximum is held in the exponent's unit (log2) and rounded up to a whole
 // number, so every rescaling is by a power of two and exact, and it is only
 // raised when it grew by more than 8 since O was last rescaled (P stays below
@@ -52,21 +52,16 @@ namespace {
 
 constexpr int CA_D = 128;
 constexpr int CA_KT = 128;  // cache tokens per step
-constexpr int CA_THREADS = 512;
+constexpr int CA_THREADS = 768;
 constexpr int CA_STAGES = 5;
 constexpr int CA_ITEMS = 4;     // items announced ahead
-constexpr int CA_READERS = 15;  // warps that read them
+constexpr int CA_READERS = 23;  // warps that read them
 constexpr uint32_t CA_HALF = 128 * 128;  // bytes of 128 rows x 64 values
 constexpr uint32_t CA_TILE = 2 * CA_HALF;
 // control block, padded to the tiles' alignment, and the tiles: 227 KB exactly
 constexpr uint32_t CA_CTL = 3072;
 constexpr size_t CA_SMEM = CA_CTL + 2 * CA_TILE + CA_STAGES * CA_TILE;
 constexpr int CA_PLAN_THREADS = 1024;
-#ifndef CA_POLY
-#define CA_POLY 0
-#endif
-constexpr float CA_P0 = 0x1.ffffe8p-1f, CA_P1 = 0x1.62e0dcp-1f, CA_P2 = 0x1.ec06dap-3f,
-                CA_P3 = 0x1.ca1446p-5f, CA_P4 = 0x1.3997d6p-7f;
 constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sums
 
 struct CaArgs {
@@ -256,14 +251,16 @@ __device__ __forceinline__ bool ca_active(int s, int j, int a, int n0) {
 struct CaCtrl {
   uint64_t full[CA_STAGES], empty[CA_STAGES];
   uint64_t qfull, qempty, vraw, drain;
-  uint64_t sfull[2], ready[2], ready2[2], corr[2], ofull[2];
+  uint64_t sfull[2], ready[2], ready2[2], corr[2], ofull[2], fread[2];
   uint64_t ifull[CA_ITEMS], iempty[CA_ITEMS];
   CaItem item[CA_ITEMS];
   uint32_t tmem;
   int abort_flag;
   int kissued, vissued, qissued;
   __nv_bfloat16 sc[2][128];      // a row's rescaling, a power of two
-  float sum[2][128], mx[2][128];  // and at an item's end its sum and maximum (log2)
+  // the row maxima of the two column halves; at an item's end a row's sum and
+  // its maximum (log2)
+  float pm[2][2][128];
 };
 
 __device__ __forceinline__ float ca_ex2(float x) {
@@ -305,28 +302,6 @@ __device__ __forceinline__ float ca_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-// 2^x of a pair on the fp32 units, for x <= 16: x = n + f with n the nearest
-// whole number (left in the low bits of x + 1.5 * 2^23) and |f| <= 1/2, 2^f by a
-// polynomial (Remez exchange on [-1/2, 1/2], relative error 2.6e-6), and n added to its
-// exponent. x below -126 gives 2^-126 instead of 0.
-__device__ __forceinline__ void ca_exp2_poly(unsigned long long x, float &e0, float &e1) {
-  float x0, x1;
-  ca_unpair(x, x0, x1);
-  x = ca_pair(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const unsigned long long big = ca_pair(12582912.f, 12582912.f);
-  const unsigned long long nbig = ca_pair(-12582912.f, -12582912.f);
-  const unsigned long long r = ca_add2(x, big);
-  const unsigned long long f = ca_fma2(ca_add2(r, nbig), ca_pair(-1.f, -1.f), x);
-  unsigned long long y = ca_fma2(f, ca_pair(CA_P4, CA_P4), ca_pair(CA_P3, CA_P3));
-  y = ca_fma2(f, y, ca_pair(CA_P2, CA_P2));
-  y = ca_fma2(f, y, ca_pair(CA_P1, CA_P1));
-  y = ca_fma2(f, y, ca_pair(CA_P0, CA_P0));
-  float r0, r1, y0, y1;
-  ca_unpair(r, r0, r1);
-  ca_unpair(y, y0, y1);
-  e0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23));
-  e1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23));
 }
 __device__ __forceinline__ void ca_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -405,6 +380,16 @@ __device__ __forceinline__ bool ca_wait_warp(uint32_t bar, uint32_t parity, vola
   if ((threadIdx.x & 31) == 0) ok = ca_wait(bar, parity, abort_flag, err);
   ok = __shfl_sync(0xffffffffu, ok, 0);
   return ok;
+}
+
+// 32 columns of a tile with masked ones (or under a scale that is not
+// positive, which is then applied here): -inf from column n on.
+__device__ __forceinline__ void ca_masked(uint32_t taddr, int n, float sl2, float (&v)[32]) {
+  tc_ld32_nowait(taddr, *reinterpret_cast<uint32_t(*)[32]>(v));
+  tc_wait_ld();
+  const float pre = sl2 > 0.f ? 1.f : sl2;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] * pre : -INFINITY;
 }
 
 // The next item of a role's warp (whole warp); false at the end or after an
@@ -511,7 +496,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   const uint32_t qfull = smem_u32(&ctl.qfull), qempty = smem_u32(&ctl.qempty);
   const uint32_t vraw = smem_u32(&ctl.vraw), drain = smem_u32(&ctl.drain);
   const uint32_t sfull = smem_u32(&ctl.sfull[0]), ready = smem_u32(&ctl.ready[0]);
-  const uint32_t ready2 = smem_u32(&ctl.ready2[0]);
+  const uint32_t ready2 = smem_u32(&ctl.ready2[0]), fread = smem_u32(&ctl.fread[0]);
   const uint32_t corr = smem_u32(&ctl.corr[0]), ofull = smem_u32(&ctl.ofull[0]);
 
   if (threadIdx.x == 0) {
@@ -533,12 +518,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       mbar_init(ready2 + 8 * s, 4);
       mbar_init(corr + 8 * s, 4);
       mbar_init(ofull + 8 * s, 1);
+      mbar_init(fread + 8 * s, 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ctl.abort_flag = 0;
     ctl.kissued = ctl.vissued = ctl.qissued = 0;
   }
-  if (warp == 12) {
+  if (warp == 20) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&ctl.tmem)),
                  "r"(512)
@@ -553,17 +539,33 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   const float sl2 = p.scale * 1.4426950408889634f;
   pdl_wait();
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    const int s = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t ts = tmem + (uint32_t)(s * 128) + ((uint32_t)((warp & 3) * 32) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    const int s = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const uint32_t ts =
+        tmem + (uint32_t)(s * 128 + half * 64) + ((uint32_t)((warp & 3) * 32) << 16);
     const float c2 = sl2 > 0.f ? sl2 : 1.f;
-    uint32_t sph = 0, oph = 0;
+    const uint32_t done = (half == 0 ? ready : ready2) + 8 * s;  // this half of P is written
+    const int pair = 1 + s * 4 + (warp & 3);  // barrier of the two warps of these rows
+    uint32_t sph = 0, fph = 0, oph = 0;
+    bool ended = false;  // an item's end that the correction warps have to read first
+    // The two warps stop together: every wait that may give up is followed by
+    // their barrier, which combines the outcomes.
+    auto both = [&](bool ok) {
+      uint32_t r;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, 64, p;\n"
+          " selp.b32 %0, 1, 0, q;\n}"
+          : "=r"(r)
+          : "r"((uint32_t)ok), "r"(pair)
+          : "memory");
+      return r != 0;
+    };
     CaItems items;
     CaItem it;
     bool ok = true;
-    while (ok && items.next(ctl, it, p.err)) {
+    while (both(ok && items.next(ctl, it, p.err))) {
       const int n0 = it.n0;
       const int tok = (it.two() ? s * p.TT : 0) + r / p.G;
       const bool valid = r < p.TT * p.G && tok < it.ntok;
@@ -573,157 +575,128 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       bool any = false;
       for (int j = it.a; j < it.b; ++j) {
         if (!ca_active(s, j, it.a, n0)) continue;
-        ok = ca_wait_all(sfull + 8 * s, sph, abort_flag, p.err);
-        if (!ok) break;
+        if (ended) {
+          ok = ca_wait_all(fread + 8 * s, fph, abort_flag, p.err);
+          fph ^= 1u;
+          ended = false;
+        }
+        ok = ok && ca_wait_all(sfull + 8 * s, sph, abort_flag, p.err);
         sph ^= 1u;
         tc_fence_after();
+        // this row's tokens of this half of the tile
+        const int nv = lim - j * CA_KT - half * 64;
+        const bool mask = __any_sync(0xffffffffu, nv < 64) || !(sl2 > 0.f);
+        float mt = -INFINITY;
+        if (!ok || !live) {
+        } else if (!mask) {
+          uint32_t u[64];
+          const float *v = reinterpret_cast<const float *>(u);
+          tc_ld32_nowait(ts, *reinterpret_cast<uint32_t(*)[32]>(u));
+          tc_ld32_nowait(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
+          tc_wait_ld();
+          float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+#pragma unroll
+          for (int i = 4; i < 60; i += 8) {
+            t0 = ca_max3(t0, v[i], v[i + 1]);
+            t1 = ca_max3(t1, v[i + 2], v[i + 3]);
+            t2 = ca_max3(t2, v[i + 4], v[i + 5]);
+            t3 = ca_max3(t3, v[i + 6], v[i + 7]);
+          }
+          t0 = ca_max3(t0, v[60], v[61]);
+          t1 = ca_max3(t1, v[62], v[63]);
+          mt = ca_max3(fmaxf(t0, t1), t2, t3);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float v[32];
+            ca_masked(ts + 32 * c, nv - 32 * c, sl2, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mt = fmaxf(mt, v[i]);
+          }
+        }
+        ctl.pm[s][half][r] = mt;
+        ok = both(ok);
+        if (!ok) break;
         if (live) {
-          const int nv = lim - j * CA_KT;  // this row's tokens of the tile
-          const bool mask = __any_sync(0xffffffffu, nv < CA_KT) || !(sl2 > 0.f);
-          // the row's new maximum, its rescaling for the correction warps, and
-          // what the exponentials subtract
-          auto grow = [&](float mt) {
-            float f = 1.f;
-            const float mt2 = ceilf(mt * c2);
-            if (mt2 > m + CA_LAZY || m == -INFINITY) {
-              f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
-              m = fmaxf(m, mt2);
-            }
-            if (any) {
+          // the row's new maximum over both halves, its rescaling for the
+          // correction warps, and what the exponentials subtract
+          mt = fmaxf(mt, ctl.pm[s][half ^ 1][r]);
+          const float mt2 = ceilf(mt * c2);
+          float f = 1.f;
+          if (mt2 > m + CA_LAZY || m == -INFINITY) {
+            f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
+            m = fmaxf(m, mt2);
+          }
+          if (any) {
+            l *= f;
+            if (half == 0) {
               ctl.sc[s][r] = __float2bfloat16_rn(valid ? f : 1.f);
-              l *= f;
               __syncwarp();
               if (lane == 0) mbar_arrive(corr + 8 * s);
             }
-            return m == -INFINITY ? 0.f : m;
-          };
-          // the first 64 columns of P are written: their product may begin
-          auto half_ready = [&]() {
-            ca_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ready + 8 * s);
-          };
-          float l0 = 0.f, l1 = 0.f;
-          if (!mask) {
-            uint32_t u[128];
-            float *v = reinterpret_cast<float *>(u);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tc_ld32_nowait(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(u + 32 * c));
-            tc_wait_ld();
-            float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
-#pragma unroll
-            for (int i = 4; i < 124; i += 8) {
-              t0 = ca_max3(t0, v[i], v[i + 1]);
-              t1 = ca_max3(t1, v[i + 2], v[i + 3]);
-              t2 = ca_max3(t2, v[i + 4], v[i + 5]);
-              t3 = ca_max3(t3, v[i + 6], v[i + 7]);
-            }
-            t0 = ca_max3(t0, v[124], v[125]);
-            t1 = ca_max3(t1, v[126], v[127]);
-            const float off = grow(ca_max3(fmaxf(t0, t1), t2, t3));
-            const unsigned long long cc = ca_pair(c2, c2), oo = ca_pair(-off, -off);
-            unsigned long long la = ca_pair(0.f, 0.f), lb = la;
-            // the exponentials in a loop over 32 columns, read again (unrolled
-            // over the row they do not stay in the instruction cache); the next
-            // columns are on their way meanwhile
-            tc_ld32_nowait(ts, *reinterpret_cast<uint32_t(*)[32]>(u));
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tc_wait_ld();
-              unsigned long long x[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                x[i] = ca_fma2(ca_pair(v[2 * i], v[2 * i + 1]), cc, oo);
-              if (c < 3) tc_ld32_nowait(ts + 32 * (c + 1), *reinterpret_cast<uint32_t(*)[32]>(u));
-              uint32_t pk[16];
-              float e[32];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                if (i % 8 < CA_POLY / 2) {
-                  ca_exp2_poly(x[i], e[2 * i], e[2 * i + 1]);
-                } else {
-                  ca_unpair(x[i], e[2 * i], e[2 * i + 1]);
-                  e[2 * i] = ca_ex2(e[2 * i]);
-                  e[2 * i + 1] = ca_ex2(e[2 * i + 1]);
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                la = ca_add2(la, ca_pair(e[2 * i], e[2 * i + 1]));
-                lb = ca_add2(lb, ca_pair(e[2 * i + 2], e[2 * i + 3]));
-              }
-              ca_st16(ts + 16 * c, pk);
-              if (c == 1) half_ready();
-            }
-            float a0, a1, b0, b1;
-            ca_unpair(la, a0, a1);
-            ca_unpair(lb, b0, b1);
-            l0 = a0 + b0;
-            l1 = a1 + b1;
-          } else {
-            // a tile with masked columns (or a scale that is not positive): two
-            // passes of 32 columns at a time
-            float mt = -INFINITY, off = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t u[32];
-              tc_ld32_nowait(ts + 32 * (c & 3), u);
-              tc_wait_ld();
-              float *v = reinterpret_cast<float *>(u);
-              const int n = nv - 32 * (c & 3);
-              const float pre = sl2 > 0.f ? 1.f : sl2;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] * pre : -INFINITY;
-              if (c < 4) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mt = fmaxf(mt, v[i]);
-                if (c == 3) off = grow(mt);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const float e0 = ca_ex2(fmaf(v[i], c2, -off));
-                  const float e1 = ca_ex2(fmaf(v[i + 1], c2, -off));
-                  l0 += e0;
-                  l1 += e1;
-                  u[i / 2] = pack_bf16x2(e0, e1);
-                }
-                ca_st16(ts + 16 * (c - 4), u);
-                if (c == 5) half_ready();
-              }
-            }
           }
-          l += l0 + l1;
+          const float off = m == -INFINITY ? 0.f : m;
+          const unsigned long long cc = ca_pair(c2, c2), oo = ca_pair(-off, -off);
+          unsigned long long la = ca_pair(0.f, 0.f), lb = la;
+          // the exponentials in a loop over 32 columns, read again (the whole
+          // row unrolled does not stay in the instruction cache); their bf16
+          // pairs overwrite columns of this half already read
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float v[32];
+            if (mask) {
+              ca_masked(ts + 32 * c, nv - 32 * c, sl2, v);
+            } else {
+              tc_ld32_nowait(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v));
+              tc_wait_ld();
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float e0, e1;
+              ca_unpair(ca_fma2(ca_pair(v[2 * i], v[2 * i + 1]), cc, oo), e0, e1);
+              e0 = ca_ex2(e0);
+              e1 = ca_ex2(e1);
+              if (i % 2 == 0) la = ca_add2(la, ca_pair(e0, e1));
+              else lb = ca_add2(lb, ca_pair(e0, e1));
+              pk[i] = pack_bf16x2(e0, e1);
+            }
+            ca_st16(ts + 16 * c, pk);
+          }
+          float a0, a1, b0, b1;
+          ca_unpair(la, a0, a1);
+          ca_unpair(lb, b0, b1);
+          l += (a0 + b0) + (a1 + b1);
           ca_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(ready2 + 8 * s);
-        } else if (lane == 0) {  // no rows here: P may hold anything
-          if (any) mbar_arrive(corr + 8 * s);
-          mbar_arrive(ready + 8 * s);
-          mbar_arrive(ready2 + 8 * s);
+        } else if (any && half == 0 && lane == 0) {  // no rows here: P may hold anything
+          mbar_arrive(corr + 8 * s);
         }
+        if (lane == 0) mbar_arrive(done);
         any = true;
       }
       if (!ok) break;
-      if (any) {  // the item's maximum and sum, for its end
-        // (its last product had the correction warps' arrival, which follows
-        // their reading of the item before)
-        ok = ca_wait_warp(ofull + 8 * s, oph, abort_flag, p.err);
-        if (!ok) break;
-        oph ^= 1u;
-        ctl.sum[s][r] = l;
-        ctl.mx[s][r] = m;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(corr + 8 * s);
+      if (any) {  // the item's sum and maximum, for its end
+        both(true);
+        if (half == 1) ctl.pm[s][1][r] = l;
+        both(true);
+        if (half == 0) {
+          // (the last product had the correction warps' arrival: they have
+          // seen the last rescaling)
+          ok = ca_wait_all(ofull + 8 * s, oph, abort_flag, p.err);
+          oph ^= 1u;
+          ctl.pm[s][0][r] = l + ctl.pm[s][1][r];
+          ctl.pm[s][1][r] = m;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(corr + 8 * s);
+        }
+        ended = true;
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ------------------------------------------------- correction and results
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const int r = (warp & 3) * 32 + lane;
     const uint32_t to = tmem + 256u + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t cph[2] = {0, 0}, oph[2] = {0, 0};
@@ -777,8 +750,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         cph[s] ^= 1u;
         oph[s] ^= 1u;
         if (!ok) continue;
-        l[s] = ctl.sum[s][r];
-        m[s] = ctl.mx[s][r];
+        l[s] = ctl.pm[s][0][r];
+        m[s] = ctl.pm[s][1][r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fread + 8 * s);
       }
       if (!ok) break;
       tc_fence_after();
@@ -854,8 +829,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 20) {
       // -------------------------------------------------------------- MMA issuer
       constexpr uint32_t IDESC_S = f16_idesc(128, 128);
       constexpr uint32_t IDESC_O = f16_idesc(128, 128) | (1u << 16);  // B = V: MN-major
@@ -938,8 +913,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             if (lead) {
 #pragma unroll
               for (int k = 4; k < 8; ++k)
-                ca_mma_ts(256 + s * 128, s * 128 + 8 * k, db + (uint64_t)((k * 2048) >> 4), IDESC_O,
-                          1u);
+                ca_mma_ts(256 + s * 128, s * 128 + 32 + 8 * k, db + (uint64_t)((k * 2048) >> 4),
+                          IDESC_O, 1u);
               if (s == s1) tc_commit(empty0 + 8 * vst);
               if (jn < b && (!two || s == 1 || jn < n0)) scores(s, s == s1, jn == b - 1);
               else tc_commit(ofull + 8 * s);  // the slot's last product
@@ -960,7 +935,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         mbar_wait(drain, 0, abort_flag, p.err, TC_DRAIN_LIMIT, false);
       }
       __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 21) {
       // ------------------------------------------------------------ Q and K tiles
       CaItems items;
       CaItem it;
@@ -1003,7 +978,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         ctl.kissued = cnt;
         ctl.qissued = nq;
       }
-    } else if (warp == 14) {
+    } else if (warp == 22) {
       // ------------------------------------------------------------------ V tiles
       CaItems items;
       CaItem it;
@@ -1100,7 +1075,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       mbar_wait(qfull, (uint32_t)((ctl.qissued - 1) & 1), abort_flag, p.err, TC_DRAIN_LIMIT, false);
   }
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
