@@ -44,6 +44,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "paged_tiles.cuh"
 #include "tc_util.cuh"
 #include "umma_desc.h"
 
@@ -56,16 +57,14 @@ constexpr int CA_THREADS = 768;
 constexpr int CA_STAGES = 5;
 constexpr int CA_ITEMS = 4;     // items announced ahead
 constexpr int CA_READERS = 23;  // warps that read them
-constexpr uint32_t CA_HALF = 128 * 128;  // bytes of 128 rows x 64 values
-constexpr uint32_t CA_TILE = 2 * CA_HALF;
 // control block, padded to the tiles' alignment, and the tiles: 227 KB exactly
 constexpr uint32_t CA_CTL = 3072;
-constexpr size_t CA_SMEM = CA_CTL + 2 * CA_TILE + CA_STAGES * CA_TILE;
+constexpr size_t CA_SMEM = CA_CTL + 2 * PT_TILE + CA_STAGES * PT_TILE;
 constexpr int CA_PLAN_THREADS = 1024;
 constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sums
 
 struct CaArgs {
-  const int32_t *block_table, *seq_lens, *row_start;
+  const int32_t *seq_lens, *row_start;
   int *hdr;          // [0] groups, [1] CTAs with work
   long long *gpre;   // [Gmax + 1] prefix of the groups' units
   int4 *ginfo;       // [2 Gmax] {seq, first row, tokens, steps}, {tokens its first row sees, L, -, -}
@@ -73,8 +72,8 @@ struct CaArgs {
   float *rec_o;      // [CTAs][2][2][128][128]
   void *out;
   float *lse;
-  int S, Nq, Gmax, Hq, Hkv, G, TT, P, box, max_pages, num_pages, out_bf16;
-  int tile_pages, tile_slots;  // a step's 128 tokens in whole pages and slots
+  PagedTiles pages;
+  int S, Nq, Gmax, Hq, Hkv, G, TT, out_bf16;
   float scale;
   unsigned *err;
 };
@@ -118,7 +117,7 @@ __global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int 
       const int r1 = a.row_start[s + 1];
       L = a.seq_lens[s];
       T = r1 - r0;
-      if (r0 < 0 || r1 < r0 || r1 > a.Nq || T > L || (long long)L > (long long)a.max_pages * a.P)
+      if (r0 < 0 || r1 < r0 || r1 > a.Nq || T > L || (long long)L > (long long)a.pages.max_pages * a.pages.P)
         raise_err(a.err, ERR_LEN);
       else
         ng = (T + GT - 1) / GT;
@@ -263,12 +262,6 @@ struct CaCtrl {
   float pm[2][2][128];
 };
 
-__device__ __forceinline__ float ca_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void ca_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -277,31 +270,6 @@ __device__ __forceinline__ void ca_st16(uint32_t taddr, const uint32_t *r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
-}
-// Two fp32 values in one register pair, and their paired operations.
-__device__ __forceinline__ unsigned long long ca_pair(float a, float b) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void ca_unpair(unsigned long long x, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ unsigned long long ca_fma2(unsigned long long a, unsigned long long b,
-                                                      unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ unsigned long long ca_add2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float ca_max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 __device__ __forceinline__ void ca_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -314,74 +282,6 @@ __device__ __forceinline__ void ca_mma_ts(uint32_t d, uint32_t a, uint64_t db, u
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(db), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void ca_tma_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
-                                          int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
-// Bounded wait, as mbar_wait, but a round may sleep up to CA_WAIT_NS until the
-// phase completes: the other warps' polling would take issue slots and
-// instruction fetches from the softmax.
-constexpr uint32_t CA_WAIT_NS = 20000, CA_WAIT_ROUNDS = 1u << 16;
-__device__ __forceinline__ bool ca_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                        unsigned *err) {
-  for (uint32_t i = 0; i < CA_WAIT_ROUNDS; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.b32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(CA_WAIT_NS)
-        : "memory");
-    if (done) return true;
-    if (*abort_flag) return false;
-  }
-  *abort_flag = 1;
-  raise_err(err, ERR_TIMEOUT);
-  return false;
-}
-
-// The same by every lane of a warp.
-__device__ __forceinline__ bool ca_wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                            unsigned *err) {
-  return __all_sync(0xffffffffu, ca_wait(bar, parity, abort_flag, err));
-}
-
-// Both of two barriers, whose checks overlap.
-__device__ __forceinline__ bool ca_wait_all2(uint32_t bar, uint32_t parity, uint32_t bar2,
-                                             uint32_t parity2, volatile int *abort_flag,
-                                             unsigned *err) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n"
-      " selp.b32 %0, 1, 0, p;\n}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(bar2), "r"(parity2)
-      : "memory");
-  if (__all_sync(0xffffffffu, done)) return true;
-  return ca_wait_all(bar, parity, abort_flag, err) && ca_wait_all(bar2, parity2, abort_flag, err);
-}
-
-__device__ __forceinline__ bool ca_elect() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
-// Whole-warp bounded wait: lane 0 polls.
-__device__ __forceinline__ bool ca_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                             unsigned *err) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = ca_wait(bar, parity, abort_flag, err);
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  return ok;
-}
-
 // 32 columns of a tile with masked ones (or under a scale that is not
 // positive, which is then applied here): -inf from column n on.
 __device__ __forceinline__ void ca_masked(uint32_t taddr, int n, float sl2, float (&v)[32]) {
@@ -398,7 +298,7 @@ struct CaItems {
   int at = 0;
   __device__ __forceinline__ bool next(CaCtrl &c, CaItem &it, unsigned *err) {
     const int i = at % CA_ITEMS;
-    if (!ca_wait_warp(smem_u32(&c.ifull[i]), (uint32_t)((at / CA_ITEMS) & 1), &c.abort_flag, err))
+    if (!wait_warp(smem_u32(&c.ifull[i]), (uint32_t)((at / CA_ITEMS) & 1), &c.abort_flag, err))
       return false;
     ++at;
     const int4 *v = reinterpret_cast<const int4 *>(&c.item[i]);
@@ -410,72 +310,6 @@ struct CaItems {
     return it.b > it.a;
   }
 };
-
-// The pieces of the steps' 128 tokens, one lane each, in step order: where
-// they lie in their pages, and the page ids, read two steps ahead. (A piece of
-// `box` tokens never crosses a page. No division per step: the loaders' few
-// instructions are on the path from a free stage to its next tile.)
-struct CaPieces {
-  static constexpr int NONE = -0x7fffffff - 1;
-  const int32_t *row;  // the sequence's block-table row, at the page read next
-  int tok, rslot, L;   // the piece read next: its first token, its slot
-  int slot;            // the slot of the step being issued
-  int id[2];
-  __device__ __forceinline__ void start(const CaArgs &p, const CaItem &it, int lane) {
-    const bool has = lane * p.box < CA_KT;
-    tok = it.a * CA_KT + (has ? lane * p.box : 0);
-    L = has ? it.L : 0;
-    const int col = tok / p.P;
-    slot = rslot = tok - col * p.P;
-    row = p.block_table + (size_t)it.seq * p.max_pages + col;
-    id[0] = read(p);
-    id[1] = read(p);
-  }
-  __device__ __forceinline__ int read(const CaArgs &p) {
-    if (tok >= L) return NONE;
-    const int v = __ldg(row);
-    tok += CA_KT;
-    rslot += p.tile_slots;
-    row += p.tile_pages;
-    if (rslot >= p.P) {
-      rslot -= p.P;
-      ++row;
-    }
-    return v;
-  }
-  // The page of this step's piece (-1: past L, or a bad page).
-  __device__ __forceinline__ int take(const CaArgs &p) {
-    int v = id[0];
-    id[0] = id[1];
-    id[1] = read(p);
-    if (v < 0 || v >= p.num_pages) {
-      if (v != NONE) raise_err(p.err, ERR_PAGE);
-      v = -1;
-    }
-    return v;
-  }
-  __device__ __forceinline__ void step(const CaArgs &p) {
-    slot += p.tile_slots;
-    if (slot >= p.P) slot -= p.P;
-  }
-};
-
-// Issues a step's tile: every piece's two halves of 64 values, by the elected
-// lane. `slot` is this lane's piece's slot in its page. Returns the bytes.
-__device__ __forceinline__ void ca_load_tile(const CaArgs &p, const CUtensorMap *map, uint32_t dst,
-                                             uint32_t bar, int page, int slot, int h, bool lead) {
-  const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
-  if (lead) mbar_arrive_expect(bar, (uint32_t)(__popc(live) * p.box * 256));
-  __syncwarp();
-  for (int i = 0, off = 0; off < CA_KT; ++i, off += p.box) {
-    const int pg = __shfl_sync(0xffffffffu, page, i), sl = __shfl_sync(0xffffffffu, slot, i);
-    if (pg >= 0 && lead) {
-      ca_tma_4d(dst + off * 128, map, bar, 0, h, sl, pg);
-      ca_tma_4d(dst + CA_HALF + off * 128, map, bar, 64, h, sl, pg);
-    }
-  }
-  __syncwarp();
-}
 
 __global__ void __launch_bounds__(CA_THREADS, 1)
     ca_attend_kernel(const __grid_constant__ CUtensorMap q_map,
@@ -491,7 +325,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     pdl_wait();
     return;
   }
-  const uint32_t ring = q_s + 2 * CA_TILE;
+  const uint32_t ring = q_s + 2 * PT_TILE;
   const uint32_t full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
   const uint32_t qfull = smem_u32(&ctl.qfull), qempty = smem_u32(&ctl.qempty);
   const uint32_t vraw = smem_u32(&ctl.vraw), drain = smem_u32(&ctl.drain);
@@ -576,11 +410,11 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       for (int j = it.a; j < it.b; ++j) {
         if (!ca_active(s, j, it.a, n0)) continue;
         if (ended) {
-          ok = ca_wait_all(fread + 8 * s, fph, abort_flag, p.err);
+          ok = wait_all(fread + 8 * s, fph, abort_flag, p.err);
           fph ^= 1u;
           ended = false;
         }
-        ok = ok && ca_wait_all(sfull + 8 * s, sph, abort_flag, p.err);
+        ok = ok && wait_all(sfull + 8 * s, sph, abort_flag, p.err);
         sph ^= 1u;
         tc_fence_after();
         // this row's tokens of this half of the tile
@@ -597,14 +431,14 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
 #pragma unroll
           for (int i = 4; i < 60; i += 8) {
-            t0 = ca_max3(t0, v[i], v[i + 1]);
-            t1 = ca_max3(t1, v[i + 2], v[i + 3]);
-            t2 = ca_max3(t2, v[i + 4], v[i + 5]);
-            t3 = ca_max3(t3, v[i + 6], v[i + 7]);
+            t0 = max3(t0, v[i], v[i + 1]);
+            t1 = max3(t1, v[i + 2], v[i + 3]);
+            t2 = max3(t2, v[i + 4], v[i + 5]);
+            t3 = max3(t3, v[i + 6], v[i + 7]);
           }
-          t0 = ca_max3(t0, v[60], v[61]);
-          t1 = ca_max3(t1, v[62], v[63]);
-          mt = ca_max3(fmaxf(t0, t1), t2, t3);
+          t0 = max3(t0, v[60], v[61]);
+          t1 = max3(t1, v[62], v[63]);
+          mt = max3(fmaxf(t0, t1), t2, t3);
         } else {
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -624,7 +458,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           const float mt2 = ceilf(mt * c2);
           float f = 1.f;
           if (mt2 > m + CA_LAZY || m == -INFINITY) {
-            f = m == -INFINITY ? (any ? 0.f : 1.f) : ca_ex2(m - mt2);
+            f = m == -INFINITY ? (any ? 0.f : 1.f) : ex2_approx(m - mt2);
             m = fmaxf(m, mt2);
           }
           if (any) {
@@ -636,8 +470,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             }
           }
           const float off = m == -INFINITY ? 0.f : m;
-          const unsigned long long cc = ca_pair(c2, c2), oo = ca_pair(-off, -off);
-          unsigned long long la = ca_pair(0.f, 0.f), lb = la;
+          const unsigned long long cc = f2_pack(c2, c2), oo = f2_pack(-off, -off);
+          unsigned long long la = f2_pack(0.f, 0.f), lb = la;
           // the exponentials in a loop over 32 columns, read again (the whole
           // row unrolled does not stay in the instruction cache); their bf16
           // pairs overwrite columns of this half already read
@@ -654,18 +488,18 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float e0, e1;
-              ca_unpair(ca_fma2(ca_pair(v[2 * i], v[2 * i + 1]), cc, oo), e0, e1);
-              e0 = ca_ex2(e0);
-              e1 = ca_ex2(e1);
-              if (i % 2 == 0) la = ca_add2(la, ca_pair(e0, e1));
-              else lb = ca_add2(lb, ca_pair(e0, e1));
+              f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), cc, oo), e0, e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              if (i % 2 == 0) la = f2_add(la, f2_pack(e0, e1));
+              else lb = f2_add(lb, f2_pack(e0, e1));
               pk[i] = pack_bf16x2(e0, e1);
             }
             ca_st16(ts + 16 * c, pk);
           }
           float a0, a1, b0, b1;
-          ca_unpair(la, a0, a1);
-          ca_unpair(lb, b0, b1);
+          f2_unpack(la, a0, a1);
+          f2_unpack(lb, b0, b1);
           l += (a0 + b0) + (a1 + b1);
           ca_wait_st();
           tc_fence_before();
@@ -684,7 +518,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         if (half == 0) {
           // (the last product had the correction warps' arrival: they have
           // seen the last rescaling)
-          ok = ca_wait_all(ofull + 8 * s, oph, abort_flag, p.err);
+          ok = wait_all(ofull + 8 * s, oph, abort_flag, p.err);
           oph ^= 1u;
           ctl.pm[s][0][r] = l + ctl.pm[s][1][r];
           ctl.pm[s][1][r] = m;
@@ -716,7 +550,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         for (int s = 0; s < 2; ++s) {
           if (!ok || !ca_active(s, j, it.a, n0)) continue;
           if (any[s]) {
-            ok = ca_wait_warp(corr + 8 * s, cph[s], abort_flag, p.err);
+            ok = wait_warp(corr + 8 * s, cph[s], abort_flag, p.err);
             if (!ok) continue;
             cph[s] ^= 1u;
             const float f = live[s] ? __bfloat162float(ctl.sc[s][r]) : 1.f;
@@ -745,8 +579,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (!any[s] || !ok) continue;
-        ok = ca_wait_warp(corr + 8 * s, cph[s], abort_flag, p.err) &&
-             ca_wait_warp(ofull + 8 * s, oph[s], abort_flag, p.err);
+        ok = wait_warp(corr + 8 * s, cph[s], abort_flag, p.err) &&
+             wait_warp(ofull + 8 * s, oph[s], abort_flag, p.err);
         cph[s] ^= 1u;
         oph[s] ^= 1u;
         if (!ok) continue;
@@ -775,8 +609,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           }
         } else {
           const float M = fmaxf(l[0] > 0.f ? m[0] : -INFINITY, l[1] > 0.f ? m[1] : -INFINITY);
-          const float e0 = l[0] > 0.f ? ca_ex2(m[0] - M) : 0.f;
-          const float e1 = l[1] > 0.f ? ca_ex2(m[1] - M) : 0.f;
+          const float e0 = l[0] > 0.f ? ex2_approx(m[0] - M) : 0.f;
+          const float e1 = l[1] > 0.f ? ex2_approx(m[1] - M) : 0.f;
           const float sum = e0 * l[0] + e1 * l[1];
           if (sum > 0.f) {
             f0 = e0 / sum;
@@ -839,25 +673,25 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       uint32_t qph = 0, rph = 0;
       int kst = 0, vst = 1;  // the stages of the next K and V tile, and their phases
       uint32_t kph = 0, vph = 0;
-      // V: 64-value halves CA_HALF apart (leading offset), 8-token groups 1024
+      // V: 64-value halves PT_HALF apart (leading offset), 8-token groups 1024
       // bytes apart
       const uint64_t q_desc = sw128_desc(q_s), k_desc = sw128_desc(ring);
-      const uint64_t v_desc = (k_desc & ~(0x3fffull << 16)) | ((uint64_t)(CA_HALF >> 4) << 16);
+      const uint64_t v_desc = (k_desc & ~(0x3fffull << 16)) | ((uint64_t)(PT_HALF >> 4) << 16);
       bool ok = true;
       // the whole warp runs this loop, so that the operands of the MMAs are
       // warp-uniform; one elected lane issues them
-      const bool lead = ca_elect();
+      const bool lead = elect_one();
       while (ok && items.next(ctl, it, p.err)) {
         const bool two = it.two();
         const int a = it.a, b = it.b, n0 = it.n0, stride = two ? 1 : 2;
         // S_s = Q_s K^T with the K tile at the ring's next even position, by
         // the elected lane
         auto scores = [&](int s, bool last_use, bool last) {
-          const uint64_t da = q_desc + (uint64_t)(two ? s * (CA_TILE >> 4) : 0);
-          const uint64_t db = k_desc + (uint64_t)(kst * (CA_TILE >> 4));
+          const uint64_t da = q_desc + (uint64_t)(two ? s * (PT_TILE >> 4) : 0);
+          const uint64_t db = k_desc + (uint64_t)(kst * (PT_TILE >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint64_t o = (uint64_t)(((k >> 2) * CA_HALF + (k & 3) * 32) >> 4);
+            const uint64_t o = (uint64_t)(((k >> 2) * PT_HALF + (k & 3) * 32) >> 4);
             tc_mma(s * 128, da + o, db + o, IDESC_S, k > 0 ? 1u : 0u);
           }
           tc_commit(sfull + 8 * s);
@@ -873,9 +707,9 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             kph ^= 1u;
           }
         };
-        ok = ca_wait_all(qfull, qph, abort_flag, p.err);
+        ok = wait_all(qfull, qph, abort_flag, p.err);
         for (int i = 0; i < (two ? 1 : 2) && ok && a + i < b; ++i) {
-          ok = ca_wait_all(full0 + 8 * kst, kph, abort_flag, p.err);
+          ok = wait_all(full0 + 8 * kst, kph, abort_flag, p.err);
           tc_fence_after();
           if (ok && lead) {
             const bool last = a + i == b - 1;
@@ -890,16 +724,16 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         for (int j = a; j < b && ok; ++j) {
           const int jn = j + stride;
           const int s0 = two ? (j < n0 ? 0 : 1) : ((j - a) & 1), s1 = two ? 1 : s0;
-          ok = ca_wait_all2(full0 + 8 * vst, vph, full0 + 8 * (jn < b ? kst : vst),
+          ok = wait_all2(full0 + 8 * vst, vph, full0 + 8 * (jn < b ? kst : vst),
                             jn < b ? kph : vph, abort_flag, p.err);
 #pragma unroll 1
           for (int s = s0; s <= s1 && ok; ++s) {
             const uint32_t ph = (rph >> s) & 1u;
-            ok = ca_wait_all(ready + 8 * s, ph, abort_flag, p.err);
+            ok = wait_all(ready + 8 * s, ph, abort_flag, p.err);
             if (!ok) break;
             rph ^= 1u << s;
             tc_fence_after();
-            const uint64_t db = v_desc + (uint64_t)(vst * (CA_TILE >> 4));
+            const uint64_t db = v_desc + (uint64_t)(vst * (PT_TILE >> 4));
             if (lead) {
               const uint32_t began = j > a + (two ? 0 : s) ? 1u : 0u;
 #pragma unroll
@@ -907,7 +741,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
                 ca_mma_ts(256 + s * 128, s * 128 + 8 * k, db + (uint64_t)((k * 2048) >> 4), IDESC_O,
                           k > 0 ? 1u : began);
             }
-            ok = ca_wait_all(ready2 + 8 * s, ph, abort_flag, p.err);
+            ok = wait_all(ready2 + 8 * s, ph, abort_flag, p.err);
             if (!ok) break;
             tc_fence_after();
             if (lead) {
@@ -939,14 +773,14 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       // ------------------------------------------------------------ Q and K tiles
       CaItems items;
       CaItem it;
-      CaPieces pieces;
-      const bool lead = ca_elect();
+      PagePieces pieces;
+      const bool lead = elect_one();
       uint32_t qph = 0, ph = 0;
       int cnt = 0, nq = 0, st = 0;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
         if (nq > 0) {
-          ok = ca_wait_warp(qempty, qph, abort_flag, p.err);
+          ok = wait_warp(qempty, qph, abort_flag, p.err);
           if (!ok) break;
           qph ^= 1u;
         }
@@ -955,18 +789,18 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           mbar_arrive_expect(qfull, (uint32_t)(tiles * 2 * p.TT * p.G * 128));
           for (int s = 0; s < tiles; ++s)
             for (int h = 0; h < 2; ++h)
-              tma_load_3d(q_s + s * CA_TILE + h * CA_HALF, &q_map, qfull, h * 64, it.h * p.G,
+              tma_load_3d(q_s + s * PT_TILE + h * PT_HALF, &q_map, qfull, h * 64, it.h * p.G,
                           it.row0 + s * p.TT);
         }
         ++nq;
-        pieces.start(p, it, lane);
+        pieces.start(p.pages, it.seq, it.L, it.a, lane);
         for (int j = it.a; j < it.b; ++j, ++cnt) {
-          const int page = pieces.take(p);
-          ok = ca_wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
+          const int page = pieces.take(p.pages);
+          ok = wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
           if (!ok) break;
-          ca_load_tile(p, &k_map, ring + st * CA_TILE, full0 + 8 * st, page, pieces.slot, it.h,
+          load_tile(p.pages, &k_map, ring + st * PT_TILE, full0 + 8 * st, page, pieces.slot, it.h,
                        lead);
-          pieces.step(p);
+          pieces.step(p.pages);
           st += 2;  // K tiles are the ring's even positions
           if (st >= CA_STAGES) {
             st -= CA_STAGES;
@@ -982,22 +816,22 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       // ------------------------------------------------------------------ V tiles
       CaItems items;
       CaItem it;
-      CaPieces pieces;
-      const bool lead = ca_elect();
+      PagePieces pieces;
+      const bool lead = elect_one();
       uint32_t vph = 0, ph = 0;
       int cnt = 0, st = 1;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
-        pieces.start(p, it, lane);
+        pieces.start(p.pages, it.seq, it.L, it.a, lane);
         for (int j = it.a; j < it.b; ++j, ++cnt) {
-          const int page = pieces.take(p);
-          ok = ca_wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
+          const int page = pieces.take(p.pages);
+          ok = wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
           if (!ok) break;
           const int nrow = it.L - j * CA_KT;  // the tile's rows that hold tokens
           const bool tail = nrow < CA_KT;
-          const uint32_t dst = ring + st * CA_TILE;
-          ca_load_tile(p, &v_map, dst, tail ? vraw : full0 + 8 * st, page, pieces.slot, it.h, lead);
-          pieces.step(p);
+          const uint32_t dst = ring + st * PT_TILE;
+          load_tile(p.pages, &v_map, dst, tail ? vraw : full0 + 8 * st, page, pieces.slot, it.h, lead);
+          pieces.step(p.pages);
           if (tail) {
             // (its own copies: waited for even after another role gave up)
             bool in = true;
@@ -1008,7 +842,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             for (int i = nrow * 8 + lane; i < CA_KT * 8; i += 32)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + h * CA_HALF +
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + h * PT_HALF +
                                                                               i * 16),
                              "r"(0)
                              : "memory");
@@ -1031,7 +865,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         bool more = w.next(true);
         for (int at = 0;; ++at) {
           const int i = at % CA_ITEMS;
-          if (!ca_wait(smem_u32(&ctl.iempty[i]), (uint32_t)((at / CA_ITEMS) & 1) ^ 1u, abort_flag,
+          if (!wait_bar(smem_u32(&ctl.iempty[i]), (uint32_t)((at / CA_ITEMS) & 1) ^ 1u, abort_flag,
                          p.err))
             break;
           CaItem &it = ctl.item[i];
@@ -1187,7 +1021,6 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   const CaLayout l = ca_layout(d, S, Nq);
   char *w = static_cast<char *>(ws);
   CaArgs a;
-  a.block_table = c.block_table;
   a.seq_lens = seq_lens;
   a.row_start = row_start;
   a.hdr = reinterpret_cast<int *>(w);
@@ -1204,38 +1037,16 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   a.Hkv = d.Hkv;
   a.G = d.Hq / d.Hkv;
   a.TT = l.TT;
-  a.P = d.P;
-  a.box = std::min(d.P & -d.P, CA_KT);  // a piece never crosses a page
-  a.tile_pages = CA_KT / d.P;
-  a.tile_slots = CA_KT % d.P;
-  a.max_pages = c.max_pages_per_seq;
-  a.num_pages = c.num_pages;
+  a.pages = paged_tiles(d, c, err);
   a.out_bf16 = out_is_bf16;
   a.scale = d.scale;
   a.err = err;
 
   CUtensorMap q_map, k_map, v_map;
-  const cuuint32_t ones[4] = {1u, 1u, 1u, 1u};
-  {
-    const cuuint64_t dims[3] = {CA_D, (cuuint64_t)d.Hq, (cuuint64_t)Nq};
-    const cuuint64_t strides[2] = {CA_D * 2, (cuuint64_t)d.Hq * CA_D * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)a.G, (cuuint32_t)a.TT};
-    if (enc(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
-            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
-  for (int i = 0; i < 2; ++i) {
-    const cuuint64_t row = (cuuint64_t)d.Hkv * CA_D * 2;
-    const cuuint64_t dims[4] = {CA_D, (cuuint64_t)d.Hkv, (cuuint64_t)d.P, (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {CA_D * 2, row, row * d.P};
-    const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)a.box, 1u};
-    if (enc(i == 0 ? &k_map : &v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            i == 0 ? c.k_pool : c.v_pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
+  if (!query_map(enc, &q_map, q, d, Nq, a.TT) ||
+      !pool_map(enc, &k_map, c.k_pool, d, c, a.pages.box) ||
+      !pool_map(enc, &v_map, c.v_pool, d, c, a.pages.box))
+    return cudaErrorInvalidValue;
   e = launch_pdl(ca_plan_kernel, 1, CA_PLAN_THREADS, 0, st, a, l.ctas);
   if (e != cudaSuccess) return e;
   e = ensure_dynamic_smem(reinterpret_cast<const void *>(ca_attend_kernel), CA_SMEM);
