@@ -25,10 +25,11 @@
 // 16 bytes a clock per SM), so prompts are bound by the exponentials: 16 a
 // clock per SM, 2,048 clocks a step of 256 x 128. One decode token per
 // sequence is bound by reading K once.
-//   warps 0-3, 4-7  the weights of K tile 0, 1 (S^T is double buffered)
-//   warp 8          issues the MMAs
-//   warp 9, 10      TMA of K tiles; of query blocks, and their LSEs
-//   warp 11         announces the items to the other warps, a few ahead
+//   warps 0-7, 8-15 the weights of the even and the odd steps (S^T is double
+//                   buffered), 4 warps for each of the two K tiles
+//   warp 16         issues the MMAs
+//   warp 17, 18     TMA of K tiles; of query blocks, and their LSEs
+//   warp 19         announces the items to the other warps, a few ahead
 // A step's sum is added to the token's sum with its rounding error carried
 // along (a token of a long prompt receives up to a million weights).
 #include <cuda.h>
@@ -44,11 +45,11 @@
 namespace qsa {
 namespace {
 
-constexpr int AM_THREADS = 384;
+constexpr int AM_THREADS = 640;
 constexpr int AM_KBUF = 2;     // pairs of K tiles
 constexpr int AM_QST = 3;      // query blocks
 constexpr int AM_ITEMS = 3;    // items announced ahead
-constexpr int AM_READERS = 11;
+constexpr int AM_READERS = 19;
 constexpr int AM_TOK = 2 * PT_ROWS;  // tokens of an item
 constexpr uint32_t AM_CTL = 3072;
 constexpr size_t AM_SMEM = AM_CTL + (size_t)(2 * AM_KBUF + AM_QST) * PT_TILE;
@@ -190,12 +191,13 @@ __device__ long long am_find(const AmArgs &p, long long at, AmItem &it) {
 struct AmCtrl {
   uint64_t kfull[AM_KBUF], kempty[AM_KBUF];
   uint64_t qfull[AM_QST], qempty[AM_QST], nfull[AM_QST], nempty[AM_QST];
-  uint64_t sfull[2], sempty[2], drain;
+  uint64_t sfull[2], sempty[2], ffull, fempty, drain;
   uint64_t ifull[AM_ITEMS], iempty[AM_ITEMS];
   AmItem item[AM_ITEMS];
   uint32_t tmem;
   int abort_flag, kissued, qissued;
   float nl[AM_QST][PT_ROWS];  // -LSE log2(e) of a query block's rows
+  float fin[AM_TOK];          // an item's sums over its odd steps
 };
 
 struct AmItems {
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   const uint32_t qfull = smem_u32(&ctl.qfull[0]), qempty = smem_u32(&ctl.qempty[0]);
   const uint32_t nfull = smem_u32(&ctl.nfull[0]), nempty = smem_u32(&ctl.nempty[0]);
   const uint32_t sfull = smem_u32(&ctl.sfull[0]), sempty = smem_u32(&ctl.sempty[0]);
+  const uint32_t ffull = smem_u32(&ctl.ffull), fempty = smem_u32(&ctl.fempty);
   const uint32_t drain = smem_u32(&ctl.drain);
 
   if (threadIdx.x == 0) {
@@ -259,6 +262,8 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       mbar_init(sempty + 8 * i, 8);
     }
     mbar_init(drain, 1);
+    mbar_init(ffull, 8);
+    mbar_init(fempty, 8);
     for (int i = 0; i < AM_ITEMS; ++i) {
       mbar_init(smem_u32(&ctl.ifull[i]), 1);
       mbar_init(smem_u32(&ctl.iempty[i]), AM_READERS);
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     ctl.abort_flag = 0;
     ctl.kissued = ctl.qissued = 0;
   }
-  if (warp == 8) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&ctl.tmem)),
                  "r"(512)
@@ -284,69 +289,74 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
   AmItem it;
   AmItems items;
   bool ok = true;
-  if (warp < 8) {
+  if (warp < 16) {
     // ---------------------------------------------------------------- weights
-    const int s = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t ts = tmem + (uint32_t)(s * 256) + ((uint32_t)((warp & 3) * 32) << 16);
+    // (this warp's steps: those of its buffer)
+    const int buf = warp >> 3, s = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const uint32_t ts =
+        tmem + (uint32_t)(s * 256 + buf * 128) + ((uint32_t)((warp & 3) * 32) << 16);
     const unsigned long long cc = f2_pack(p.c2, p.c2);
-    int buf = 0, st = 0;
-    uint32_t sph = 0, nph = 0;
+    int turn = 0, st = 0;
+    uint32_t sph = 0, nph = 0, fph = 0;
     while (ok && items.next(ctl, it, p.err)) {
       const int t = it.u * AM_TOK + s * PT_ROWS + r;  // this thread's token
       const int before = it.L - it.T;                 // tokens before the chunk
       float sum = 0.f, lost = 0.f;
       int qb = it.q0 + it.a % it.nq;
       for (int k = it.a; k < it.b; ++k) {
-        ok = wait_all2(sfull + 8 * buf, sph, nfull + 8 * st, nph, abort_flag, p.err);
-        if (!ok) break;
-        tc_fence_after();
         const int cols = am_cols(p, it.T, qb);
-        // the first column that sees the token: row i sees its first before + i + 1
-        const int c0 = (t - before - qb * p.TT) * p.G;
-        const bool mask = __any_sync(0xffffffffu, c0 > 0) || (cols & 31) != 0;
-        unsigned long long la = f2_pack(0.f, 0.f), lb = la;
-        const float *nl = ctl.nl[st];
-        const int chunks = (cols + 31) >> 5;
+        const bool mine = turn == buf;
+        if (mine) {
+          ok = wait_all2(sfull + 8 * buf, sph, nfull + 8 * st, nph, abort_flag, p.err);
+          if (!ok) break;
+          sph ^= 1u;
+          tc_fence_after();
+          // the first column that sees the token: row i sees its first before + i + 1
+          const int c0 = (t - before - qb * p.TT) * p.G;
+          const bool mask = __any_sync(0xffffffffu, c0 > 0) || (cols & 31) != 0;
+          unsigned long long la = f2_pack(0.f, 0.f), lb = la;
+          const float *nl = ctl.nl[st];
+          const int chunks = (cols + 31) >> 5;
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          uint32_t u[32];
-          const float *v = reinterpret_cast<const float *>(u);
-          tc_ld32_nowait(ts + buf * 128 + 32 * c, u);
-          tc_wait_ld();
-          float e[32];
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t u[32];
+            const float *v = reinterpret_cast<const float *>(u);
+            tc_ld32_nowait(ts + 32 * c, u);
+            tc_wait_ld();
+            float e[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 n = *reinterpret_cast<const float4 *>(nl + 32 * c + i);
-            f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), cc, f2_pack(n.x, n.y)), e[i], e[i + 1]);
-            f2_unpack(f2_fma(f2_pack(v[i + 2], v[i + 3]), cc, f2_pack(n.z, n.w)), e[i + 2],
-                      e[i + 3]);
-          }
-          if (mask) {
+            for (int i = 0; i < 32; i += 4) {
+              const float4 n = *reinterpret_cast<const float4 *>(nl + 32 * c + i);
+              f2_unpack(f2_fma(f2_pack(v[i], v[i + 1]), cc, f2_pack(n.x, n.y)), e[i], e[i + 1]);
+              f2_unpack(f2_fma(f2_pack(v[i + 2], v[i + 3]), cc, f2_pack(n.z, n.w)), e[i + 2],
+                        e[i + 3]);
+            }
+            if (mask) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i < c0 || 32 * c + i >= cols) e[i] = -INFINITY;
-          }
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i < c0 || 32 * c + i >= cols) e[i] = -INFINITY;
+            }
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            la = f2_add(la, f2_pack(ex2_approx(e[i]), ex2_approx(e[i + 1])));
-            lb = f2_add(lb, f2_pack(ex2_approx(e[i + 2]), ex2_approx(e[i + 3])));
+            for (int i = 0; i < 32; i += 4) {
+              la = f2_add(la, f2_pack(ex2_approx(e[i]), ex2_approx(e[i + 1])));
+              lb = f2_add(lb, f2_pack(ex2_approx(e[i + 2]), ex2_approx(e[i + 3])));
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(sempty + 8 * buf);
+            mbar_arrive(nempty + 8 * st);
+          }
+          float a0, a1, b0, b1;
+          f2_unpack(la, a0, a1);
+          f2_unpack(lb, b0, b1);
+          // the sum with what its last rounding lost
+          const float y = __fsub_rn((a0 + b0) + (a1 + b1), lost), z = __fadd_rn(sum, y);
+          lost = __fsub_rn(__fsub_rn(z, sum), y);
+          sum = z;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(sempty + 8 * buf);
-          mbar_arrive(nempty + 8 * st);
-        }
-        float a0, a1, b0, b1;
-        f2_unpack(la, a0, a1);
-        f2_unpack(lb, b0, b1);
-        // the sum with what its last rounding lost
-        const float y = __fsub_rn((a0 + b0) + (a1 + b1), lost), z = __fadd_rn(sum, y);
-        lost = __fsub_rn(__fsub_rn(z, sum), y);
-        sum = z;
-        buf ^= 1;
-        if (buf == 0) sph ^= 1u;
+        turn ^= 1;
         if (++st == AM_QST) {
           st = 0;
           nph ^= 1u;
@@ -354,6 +364,22 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
         if (++qb == it.q0 + it.nq) qb = it.q0;
       }
       if (!ok) break;
+      // the sums over both buffers' steps; fin is read before it is written again
+      if (buf == 1) {
+        ok = wait_all(fempty, fph ^ 1u, abort_flag, p.err);
+        fph ^= 1u;
+        if (!ok) break;
+        ctl.fin[s * PT_ROWS + r] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ffull);
+        continue;
+      }
+      ok = wait_all(ffull, fph, abort_flag, p.err);
+      fph ^= 1u;
+      if (!ok) break;
+      sum += ctl.fin[s * PT_ROWS + r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(fempty);
       float v = t < it.L ? sum : 0.f;  // (slots past L hold anything)
       v += __shfl_xor_sync(0xffffffffu, v, 1);
       v += __shfl_xor_sync(0xffffffffu, v, 2);
@@ -364,7 +390,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           p.rec[((size_t)blockIdx.x * 2 + (it.a == 0 ? 1 : 0)) * 64 + s * 32 + (r >> 2)] = v;
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // -------------------------------------------------------------- MMA issuer
     const bool lead = elect_one();
     const uint64_t k_desc = sw128_desc(k_s), q_desc = sw128_desc(q_s);
@@ -416,7 +442,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       mbar_wait(drain, 0, abort_flag, p.err, TC_DRAIN_LIMIT, false);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---------------------------------------------------------------- K tiles
     const bool lead = elect_one();
     int kb = 0, cnt = 0;
@@ -447,7 +473,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       }
     }
     if (lane == 0) ctl.kissued = cnt;
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // ------------------------------------------------- query blocks, their LSEs
     const bool lead = elect_one();
     int st = 0, cnt = 0;
@@ -549,7 +575,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     }
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
