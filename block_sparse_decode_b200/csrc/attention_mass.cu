@@ -54,6 +54,7 @@ constexpr int AM_TOK = 2 * PT_ROWS;  // tokens of an item
 constexpr uint32_t AM_CTL = 3072;
 constexpr size_t AM_SMEM = AM_CTL + (size_t)(2 * AM_KBUF + AM_QST) * PT_TILE;
 constexpr int AM_PLAN_THREADS = 1024;
+constexpr int AM_POLY = 2;  // of 8 pairs of exponentials, those on the fp32 units
 constexpr int AM_FEW = 4;  // chunk tokens that are loaded one by one
 
 struct AmArgs {
@@ -188,6 +189,32 @@ __device__ long long am_find(const AmArgs &p, long long at, AmItem &it) {
 
 // ------------------------------------------------------------------ weigh
 
+// 2^x of a pair on the fp32 units, for x < 128: x = n + f with n the nearest
+// whole number (left in the low bits of x + 1.5 * 2^23) and |f| <= 1/2, 2^f by
+// the degree-5 polynomial of least relative error there (Remez exchange; 2.4e-7
+// with its fp32 roundings), and n added to its exponent. x below -126 counts
+// as -126: its weight, at most 2^-126, is 0 instead of that.
+__device__ __forceinline__ unsigned long long exp2_poly(unsigned long long x) {
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  const float m0 = fmaxf(x0, -126.f), m1 = fmaxf(x1, -126.f);
+  const unsigned long long m = f2_pack(m0, m1);
+  const unsigned long long r = f2_add(m, f2_pack(12582912.f, 12582912.f));
+  const unsigned long long f =
+      f2_fma(f2_add(r, f2_pack(-12582912.f, -12582912.f)), f2_pack(-1.f, -1.f), m);
+  unsigned long long y = f2_fma(f, f2_pack(0x1.5c08e6p-10f, 0x1.5c08e6p-10f),
+                                f2_pack(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
+  y = f2_fma(f, y, f2_pack(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
+  y = f2_fma(f, y, f2_pack(0x1.ebf918p-3f, 0x1.ebf918p-3f));
+  y = f2_fma(f, y, f2_pack(0x1.62e428p-1f, 0x1.62e428p-1f));
+  y = f2_fma(f, y, f2_pack(0x1.000002p+0f, 0x1.000002p+0f));
+  float r0, r1, y0, y1;
+  f2_unpack(r, r0, r1);
+  f2_unpack(y, y0, y1);
+  return f2_pack(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23)),
+                 __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23)));
+}
+
 struct AmCtrl {
   uint64_t kfull[AM_KBUF], kempty[AM_KBUF];
   uint64_t qfull[AM_QST], qempty[AM_QST], nfull[AM_QST], nempty[AM_QST];
@@ -313,12 +340,13 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           tc_fence_after();
           // the first column that sees the token: row i sees its first before + i + 1
           const int c0 = (t - before - qb * p.TT) * p.G;
-          const bool mask = __any_sync(0xffffffffu, c0 > 0) || (cols & 31) != 0;
+          // (lanes are consecutive tokens: the warp's least and largest)
+          const int cmin = __shfl_sync(0xffffffffu, c0, 0), cmax = cmin + 31 * p.G;
           unsigned long long la = f2_pack(0.f, 0.f), lb = la;
           const float *nl = ctl.nl[st];
           const int chunks = (cols + 31) >> 5;
 #pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
+          for (int c = max(0, cmin) >> 5; c < chunks; ++c) {
             uint32_t u[32];
             const float *v = reinterpret_cast<const float *>(u);
             tc_ld32_nowait(ts + 32 * c, u);
@@ -331,15 +359,19 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
               f2_unpack(f2_fma(f2_pack(v[i + 2], v[i + 3]), cc, f2_pack(n.z, n.w)), e[i + 2],
                         e[i + 3]);
             }
-            if (mask) {
+            if (32 * c < cmax || 32 * c + 32 > cols) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (32 * c + i < c0 || 32 * c + i >= cols) e[i] = -INFINITY;
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              la = f2_add(la, f2_pack(ex2_approx(e[i]), ex2_approx(e[i + 1])));
-              lb = f2_add(lb, f2_pack(ex2_approx(e[i + 2]), ex2_approx(e[i + 3])));
+              la = f2_add(la, (i / 2) % 8 < AM_POLY
+                                  ? exp2_poly(f2_pack(e[i], e[i + 1]))
+                                  : f2_pack(ex2_approx(e[i]), ex2_approx(e[i + 1])));
+              lb = f2_add(lb, (i / 2 + 1) % 8 < AM_POLY
+                                  ? exp2_poly(f2_pack(e[i + 2], e[i + 3]))
+                                  : f2_pack(ex2_approx(e[i + 2]), ex2_approx(e[i + 3])));
             }
           }
           tc_fence_before();
@@ -478,17 +510,32 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
     const bool lead = elect_one();
     int st = 0, cnt = 0;
     uint32_t ph = 1;
+    // this lane's columns lane + 32 i: where their LSEs lie from the block's
+    // first row on, and the values of the next step, read one step ahead
+    int off[4];
+    float n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      off[i] = (lane + 32 * i) / p.G * p.Hq + (lane + 32 * i) % p.G;
+    auto read = [&](int h, int qb) {
+      const int cols = am_cols(p, it.T, qb);
+      const float *l = p.lse + (size_t)(it.r0 + qb * p.TT) * p.Hq + h * p.G;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n[i] = lane + 32 * i < cols ? __ldg(l + off[i]) : INFINITY;
+    };
     while (ok && items.next(ctl, it, p.err)) {
       int h = it.a / it.nq, qb = it.q0 + it.a % it.nq;
+      read(h, qb);
       for (int k = it.a; k < it.b; ++k) {
-        const int cols = am_cols(p, it.T, qb), row = it.r0 + qb * p.TT;
-        float n[4];
+        const int cols = am_cols(p, it.T, qb), row = it.r0 + qb * p.TT, hk = h;
+        float nl[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = lane + 32 * i;
-          n[i] = c < cols ? __ldg(p.lse + (size_t)(row + c / p.G) * p.Hq + h * p.G + c % p.G)
-                          : INFINITY;
+        for (int i = 0; i < 4; ++i) nl[i] = n[i];
+        if (++qb == it.q0 + it.nq) {
+          qb = it.q0;
+          ++h;
         }
+        if (k + 1 < it.b) read(h, qb);
         ok = wait_all2(qempty + 8 * st, ph, nempty + 8 * st, ph, abort_flag, p.err);
         if (!ok) break;
         if (lead) {
@@ -498,12 +545,12 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             mbar_arrive_expect(bar, (uint32_t)(cols * 256));
             for (int i = 0; i < toks; ++i)
               for (int x = 0; x < 2; ++x)
-                tma_load_3d(dst + x * PT_HALF + i * p.G * 128, &q1_map, bar, x * 64, h * p.G,
+                tma_load_3d(dst + x * PT_HALF + i * p.G * 128, &q1_map, bar, x * 64, hk * p.G,
                             row + i);
           } else {
             mbar_arrive_expect(bar, (uint32_t)(p.TT * p.G * 256));
             for (int x = 0; x < 2; ++x)
-              tma_load_3d(dst + x * PT_HALF, &q_map, bar, x * 64, h * p.G, row);
+              tma_load_3d(dst + x * PT_HALF, &q_map, bar, x * 64, hk * p.G, row);
           }
         }
         __syncwarp();
@@ -511,17 +558,13 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           ctl.nl[st][lane + 32 * i] =
-              n[i] == -INFINITY ? -INFINITY : -n[i] * 1.4426950408889634f;
+              nl[i] == -INFINITY ? -INFINITY : -nl[i] * 1.4426950408889634f;
         __syncwarp();
         if (lane == 0) mbar_arrive(nfull + 8 * st);
         ++cnt;
         if (++st == AM_QST) {
           st = 0;
           ph ^= 1u;
-        }
-        if (++qb == it.q0 + it.nq) {
-          qb = it.q0;
-          ++h;
         }
       }
     }

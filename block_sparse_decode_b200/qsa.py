@@ -119,8 +119,14 @@ def _check(status: int):
         raise QsaError(status, lib().qsa_last_error().decode())
 
 
+# the current stream's handle without building a Stream object (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -492,7 +498,7 @@ def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda"
 def _on_current_device(t, stream):
     """The calls launch on the current device (or on the device of an explicit
     stream, which the caller has made current)."""
-    if stream is None and t.is_cuda and t.device.index != torch.cuda.current_device():
+    if stream is None and t.is_cuda and t.get_device() != torch.cuda.current_device():
         raise ValueError(f"tensors are on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 
@@ -538,7 +544,7 @@ def qsa_qk_norm_rope(pos, q, k, q_weight, k_weight, eps: float, rope, q_out, k_o
 
 
 def _shape(t, shape, name):
-    if t is None or tuple(t.shape) != tuple(shape):
+    if t is None or t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got "
                          f"{None if t is None else tuple(t.shape)}")
 
