@@ -27,9 +27,10 @@
 //   warps 16-19     rescale O where a maximum grew; at an item's end read O
 //                   and write the result
 //   warp 20         issues the MMAs
-//   warp 21, 22     TMA of Q and K tiles; of V tiles, whose rows past L_s are
-//                   set to zero (0 * NaN in a stale slot would reach the sum)
-//   warp 23         announces the items to the other warps, a few ahead
+//   warp 21, 22     TMA of K tiles; of V tiles, whose rows past L_s are set to
+//                   zero (0 * NaN in a stale slot would reach the sum)
+//   warp 23         announces the items to the other warps, one or two ahead,
+//                   and loads their query tiles
 // The maximum is held in the exponent's unit (log2) and rounded up to a whole
 // number, so every rescaling is by a power of two and exact, and it is only
 // raised when it grew by more than 8 since O was last rescaled (P stays below
@@ -423,22 +424,27 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         float mt = -INFINITY;
         if (!ok || !live) {
         } else if (!mask) {
-          uint32_t u[64];
-          const float *v = reinterpret_cast<const float *>(u);
-          tc_ld32_nowait(ts, *reinterpret_cast<uint32_t(*)[32]>(u));
-          tc_ld32_nowait(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
-          tc_wait_ld();
-          float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float v[32];
+            tc_ld32_nowait(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v));
+            tc_wait_ld();
+            float t0 = mt, t1 = v[0], t2 = v[1], t3 = v[2];
+            t0 = max3(t0, v[3], v[4]);
+            t1 = max3(t1, v[5], v[6]);
+            t2 = max3(t2, v[7], v[8]);
+            t3 = max3(t3, v[9], v[10]);
+            t0 = max3(t0, v[11], v[12]);
+            t1 = max3(t1, v[13], v[14]);
 #pragma unroll
-          for (int i = 4; i < 60; i += 8) {
-            t0 = max3(t0, v[i], v[i + 1]);
-            t1 = max3(t1, v[i + 2], v[i + 3]);
-            t2 = max3(t2, v[i + 4], v[i + 5]);
-            t3 = max3(t3, v[i + 6], v[i + 7]);
+            for (int i = 15; i < 31; i += 8) {
+              t0 = max3(t0, v[i], v[i + 1]);
+              t1 = max3(t1, v[i + 2], v[i + 3]);
+              t2 = max3(t2, v[i + 4], v[i + 5]);
+              t3 = max3(t3, v[i + 6], v[i + 7]);
+            }
+            mt = max3(max3(t0, t1, v[31]), t2, t3);
           }
-          t0 = max3(t0, v[60], v[61]);
-          t1 = max3(t1, v[62], v[63]);
-          mt = max3(fmaxf(t0, t1), t2, t3);
         } else {
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -530,30 +536,32 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     }
   } else if (warp < 20) {
     // ------------------------------------------------- correction and results
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int r = (warp & 3) * 32 + lane;
     const uint32_t to = tmem + 256u + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t cph[2] = {0, 0}, oph[2] = {0, 0};
+    uint32_t cph = 0, oph = 0;  // a bit per slot
     CaItems items;
     CaItem it;
     bool ok = true;
     while (ok && items.next(ctl, it, p.err)) {
       const int n0 = it.n0;
-      bool any[2] = {false, false};
-      bool live[2];  // whether the softmax warp of these rows has any of the item's
-#pragma unroll
+      // bits per slot: it had a step; the softmax warps of these rows have any
+      // of the item's
+      uint32_t any = 0, live = 0;
+#pragma unroll 1
       for (int s = 0; s < 2; ++s)
-        live[s] = __any_sync(0xffffffffu, r < p.TT * p.G &&
-                                              (it.two() ? s * p.TT : 0) + r / p.G < it.ntok);
+        if (__any_sync(0xffffffffu, r < p.TT * p.G &&
+                                        (it.two() ? s * p.TT : 0) + r / p.G < it.ntok))
+          live |= 1u << s;
       for (int j = it.a; j < it.b && ok; ++j) {
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < 2; ++s) {
           if (!ok || !ca_active(s, j, it.a, n0)) continue;
-          if (any[s]) {
-            ok = wait_warp(corr + 8 * s, cph[s], abort_flag, p.err);
+          if ((any >> s) & 1u) {
+            ok = wait_all(corr + 8 * s, (cph >> s) & 1u, abort_flag, p.err);
             if (!ok) continue;
-            cph[s] ^= 1u;
-            const float f = live[s] ? __bfloat162float(ctl.sc[s][r]) : 1.f;
+            cph ^= 1u << s;
+            const float f = (live >> s) & 1u ? __bfloat162float(ctl.sc[s][r]) : 1.f;
             if (__any_sync(0xffffffffu, f != 1.f)) {
               tc_fence_after();
 #pragma unroll 1
@@ -567,7 +575,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
               ca_wait_st();
             }
           }
-          any[s] = true;
+          any |= 1u << s;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(ready + 8 * s);
@@ -578,11 +586,11 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       float l[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        if (!any[s] || !ok) continue;
-        ok = wait_warp(corr + 8 * s, cph[s], abort_flag, p.err) &&
-             wait_warp(ofull + 8 * s, oph[s], abort_flag, p.err);
-        cph[s] ^= 1u;
-        oph[s] ^= 1u;
+        if (!((any >> s) & 1u) || !ok) continue;
+        ok = wait_all2(corr + 8 * s, (cph >> s) & 1u, ofull + 8 * s, (oph >> s) & 1u, abort_flag,
+                       p.err);
+        cph ^= 1u << s;
+        oph ^= 1u << s;
         if (!ok) continue;
         l[s] = ctl.pm[s][0][r];
         m[s] = ctl.pm[s][1][r];
@@ -618,8 +626,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             lse = (M + log2f(sum)) * 0.6931471805599453f;
           }
         }
-        const bool has = two ? (s == 0 ? any[0] : any[1]) : true;
-        const bool has1 = !two && any[1];
+        const bool has = !two || ((any >> s) & 1u);
+        const bool has1 = !two && (any & 2u);
         const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
         const size_t rec = ((size_t)blockIdx.x * 2 + piece) * 256 + s * 128 + r;
         if (valid) {
@@ -628,42 +636,53 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         }
         if (!has) continue;
         const uint32_t ta = to + (two ? s * 128 : 0);
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          float o[16];
-          tc_ld16(ta + 16 * c, o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
-          if (has1) {
-            float o1[16];
-            tc_ld16(to + 128 + 16 * c, o1);
-            if (f1 > 0.f) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = fmaf(o1[i], f1, o[i]);
-            }
-          }
-          if (!valid) continue;
+        auto put = [&](const float *o, int col, int n) {  // n values from column col on
+          if (!valid) return;
           if (whole && p.out_bf16) {
             uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D +
-                                                 16 * c);
+                                                 col);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < n / 8; ++i)
               d[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
                                 pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
                                 pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
                                 pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
           } else {
             float4 *d = reinterpret_cast<float4 *>(
-                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + 16 * c);
+                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + col);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < n / 4; ++i)
               d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        };
+        if (!has1) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            tc_ld32_nowait(ta + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
+            put(o, 32 * c, 32);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float o[16], o1[16];
+            tc_ld16(ta + 16 * c, o);
+            tc_ld16(to + 128 + 16 * c, o1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
+              if (f1 > 0.f) o[i] = fmaf(o1[i], f1, o[i]);
+            }
+            put(o, 16 * c, 16);
           }
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 20) {
       // -------------------------------------------------------------- MMA issuer
       constexpr uint32_t IDESC_S = f16_idesc(128, 128);
@@ -770,29 +789,15 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 21) {
-      // ------------------------------------------------------------ Q and K tiles
+      // ------------------------------------------------------------------ K tiles
       CaItems items;
       CaItem it;
       PagePieces pieces;
       const bool lead = elect_one();
-      uint32_t qph = 0, ph = 0;
-      int cnt = 0, nq = 0, st = 0;
+      uint32_t ph = 0;
+      int cnt = 0, st = 0;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
-        if (nq > 0) {
-          ok = wait_warp(qempty, qph, abort_flag, p.err);
-          if (!ok) break;
-          qph ^= 1u;
-        }
-        if (lead) {
-          const int tiles = it.two() ? 2 : 1;
-          mbar_arrive_expect(qfull, (uint32_t)(tiles * 2 * p.TT * p.G * 128));
-          for (int s = 0; s < tiles; ++s)
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(q_s + s * PT_TILE + h * PT_HALF, &q_map, qfull, h * 64, it.h * p.G,
-                          it.row0 + s * p.TT);
-        }
-        ++nq;
         pieces.start(p.pages, it.seq, it.L, it.a, lane);
         for (int j = it.a; j < it.b; ++j, ++cnt) {
           const int page = pieces.take(p.pages);
@@ -808,10 +813,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           }
         }
       }
-      if (lane == 0) {
-        ctl.kissued = cnt;
-        ctl.qissued = nq;
-      }
+      if (lane == 0) ctl.kissued = cnt;
     } else if (warp == 22) {
       // ------------------------------------------------------------------ V tiles
       CaItems items;
@@ -859,7 +861,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       }
       if (lane == 0) ctl.vissued = cnt;
     } else {
-      // ------------------------------------------------------- the items, ahead
+      // -------------------------------------- the items, ahead, and their Q tiles
       if (lane == 0) {
         CaWalk w(p, blockIdx.x);
         bool more = w.next(true);
@@ -884,6 +886,16 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           }
           mbar_arrive(smem_u32(&ctl.ifull[i]));
           if (!more) break;
+          // the item's query tiles, once the one before it has used its own
+          // (its K and V tiles are on their way already)
+          if (at > 0 && !wait_bar(qempty, (uint32_t)(at - 1) & 1u, abort_flag, p.err)) break;
+          const int tiles = w.w == 2 ? 2 : 1;
+          mbar_arrive_expect(qfull, (uint32_t)(tiles * 2 * p.TT * p.G * 128));
+          for (int s = 0; s < tiles; ++s)
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(q_s + s * PT_TILE + h * PT_HALF, &q_map, qfull, h * 64, w.h * p.G,
+                          w.gi.y + s * p.TT);
+          ctl.qissued = at + 1;
           more = w.next(false);
         }
       }
