@@ -1065,7 +1065,7 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   if (e != cudaSuccess) return e;
   e = launch_pdl(ca_attend_kernel, l.ctas, CA_THREADS, CA_SMEM, st, q_map, k_map, v_map, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ca_join_kernel, dim3(l.ctas, 4), 256, 0, st, a);
+  return launch_pdl(ca_join_kernel, dim3(l.ctas, 12), 256, 0, st, a);
 }
 
 }  // namespace qsa
