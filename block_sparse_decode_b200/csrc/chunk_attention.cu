@@ -62,11 +62,16 @@ constexpr int CA_READERS = 23;  // warps that read them
 constexpr uint32_t CA_CTL = 3072;
 constexpr size_t CA_SMEM = CA_CTL + 2 * PT_TILE + CA_STAGES * PT_TILE;
 constexpr int CA_PLAN_THREADS = 1024;
+// An item's start (queries, first tiles, its result) counts as this many steps
+// where a CTA has at least CA_MANY units: ragged chunks 327 us without, 280, 247,
+// 254 and 253 with 2, 3, 4 and 6. (With fewer, every CTA gets a step or two: a
+// single sequence's time is latency.)
+constexpr int CA_START = 3, CA_MANY = 16;
 constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sums
 
 struct CaArgs {
   const int32_t *seq_lens, *row_start;
-  int *hdr;          // [0] groups, [1] CTAs with work
+  int *hdr;          // [0] groups, [1] CTAs with work, [2] steps that an item's start counts as
   long long *gpre;   // [Gmax + 1] prefix of the groups' units
   int4 *ginfo;       // [2 Gmax] {seq, first row, tokens, steps}, {tokens its first row sees, L, -, -}
   float *rec_lse;    // [CTAs][2][2][128]
@@ -141,13 +146,24 @@ __global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int 
   }
   const int G = (int)min(gbase, (long long)a.Gmax);
   __syncthreads();
+  // the groups' steps, to see whether there are enough to count the items'
+  // starts too
+  long long work = 0;
+  for (int base = 0; base < G; base += CA_PLAN_THREADS) {
+    const int g = base + tid;
+    long long n = 0, tot;
+    if (g < G) n = (long long)a.Hkv * a.ginfo[2 * g].w * ca_weight(a.ginfo[2 * g].z, a.TT);
+    ca_scan(n, wsum, &tot);
+    work += tot;
+  }
+  const int start = work >= (long long)CA_MANY * ctas ? CA_START : 0;
   long long tbase = 0;
   for (int base = 0; base < G; base += CA_PLAN_THREADS) {
     const int g = base + tid;
     long long n = 0;
     if (g < G) {
       const int4 gi = a.ginfo[2 * g];
-      n = (long long)a.Hkv * gi.w * ca_weight(gi.z, a.TT);
+      n = (long long)a.Hkv * (gi.w + start) * ca_weight(gi.z, a.TT);
     }
     long long tot;
     const long long off = tbase + ca_scan(n, wsum, &tot);
@@ -157,9 +173,10 @@ __global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int 
   if (tid == 0) {
     a.gpre[G] = tbase;
     a.hdr[0] = G;
-    // every range holds at least two units, so every CTA inside an item's
-    // range has a step of it
-    a.hdr[1] = (int)min((long long)ctas, max(1LL, tbase / 2));
+    // every range is at least as long as the units between two steps, so every
+    // CTA inside an item's range has a step of it
+    a.hdr[1] = (int)min((long long)ctas, max(1LL, tbase / (2 * (start + 1))));
+    a.hdr[2] = start;
   }
 }
 
@@ -176,11 +193,13 @@ __device__ __forceinline__ int ca_owner(long long total, long long unit, int n) 
   return c;
 }
 
-// The items of one CTA's range, in order. Units are counted from the range's
-// start, which keeps them in 32 bits.
+// The items of one CTA's range, in order. An item of n steps has w (start + n)
+// units: with many steps in all, an item's start (queries, first tiles, its
+// result) counts as CA_START steps. Units are counted from the range's start,
+// which keeps them in 32 bits.
 struct CaWalk {
   int u, hi;  // the item's first unit (before 0: it began in an earlier CTA), the range's end
-  int g, h, w;
+  int g, h, w, start;
   int4 gi;  // {seq, first row, tokens, steps}
   int lim0, L;
   int a, b;  // this CTA's steps of the item
@@ -188,9 +207,10 @@ struct CaWalk {
 
   __device__ CaWalk(const CaArgs &args, int c) : p(args) {
     const int n = p.hdr[1], G = p.hdr[0];
-    u = hi = g = h = 0;
+    u = hi = g = h = start = 0;
     w = 1;
     if (G == 0 || c >= n) return;
+    start = p.hdr[2];
     const long long total = p.gpre[G], lo = ca_bound(total, c, n);
     hi = (int)(ca_bound(total, c + 1, n) - lo);
     int x = 0, y = G - 1;  // last group that starts at or before lo
@@ -200,7 +220,7 @@ struct CaWalk {
     }
     g = x;
     load();
-    const long long u0 = p.gpre[g], per = (long long)w * gi.w;
+    const long long u0 = p.gpre[g], per = (long long)w * (gi.w + start);
     h = (int)((lo - u0) / per);
     u = (int)(u0 + h * per - lo);
   }
@@ -216,7 +236,7 @@ struct CaWalk {
   __device__ bool next(bool first) {
     for (;;) {
       if (!first) {
-        u += w * gi.w;
+        u += w * (gi.w + start);
         if (u >= hi) return false;
         if (++h == p.Hkv) {
           h = 0;
@@ -226,8 +246,9 @@ struct CaWalk {
       }
       first = false;
       if (u >= hi) return false;
-      a = u < 0 ? (-u + w - 1) / w : 0;
-      b = min(gi.w, (hi - u + w - 1) / w);
+      // step 0 begins at the item's first unit, step j at unit w (start + j)
+      a = u < 0 ? max(1, (-u + w - 1) / w - start) : 0;
+      b = min(gi.w, max(1, (hi - u + w - 1) / w - start));
       if (a < b) return true;
     }
   }
@@ -256,7 +277,8 @@ struct CaCtrl {
   CaItem item[CA_ITEMS];
   uint32_t tmem;
   int abort_flag;
-  int kissued, vissued, qissued;
+  int qissued;
+  int last[CA_STAGES];  // the phase of a stage's last tile (+ 2: there is one)
   __nv_bfloat16 sc[2][128];      // a row's rescaling, a power of two
   // the row maxima of the two column halves; at an item's end a row's sum and
   // its maximum (log2)
@@ -292,6 +314,31 @@ __device__ __forceinline__ void ca_masked(uint32_t taddr, int n, float sl2, floa
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] * pre : -INFINITY;
 }
+
+// The ring of K and V tiles is filled in the order in which the MMAs use it.
+// Two tiles: K_0 V_0 K_1 V_1 ... One tile, whose slots work on two steps at a
+// time: K_0 K_1 V_0 K_2 V_1 ... K_{n-1} V_{n-2} V_{n-1}. Distance from tile i of
+// an item's n to the next one of its kind (after the last: to the next item),
+// and of the first V tile from the item's start.
+__device__ __forceinline__ int ca_next_k(bool two, int i, int n) {
+  return two ? 2 : i == n - 1 ? (n == 1 ? 2 : 3) : i == 0 ? 1 : 2;
+}
+__device__ __forceinline__ int ca_next_v(bool two, int i, int n) {
+  return i == n - 1 ? 1 : !two && i == n - 2 ? 1 : 2;
+}
+__device__ __forceinline__ int ca_first_v(bool two, int n) { return two || n == 1 ? 1 : 2; }
+// A place in the ring: stage and phase.
+struct CaPlace {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void move(int d) {
+    st += d;
+    if (st >= CA_STAGES) {
+      st -= CA_STAGES;
+      ph ^= 1u;
+    }
+  }
+};
 
 // The next item of a role's warp (whole warp); false at the end or after an
 // abort. Its fields are in registers afterwards and its slot is given back.
@@ -357,7 +404,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ctl.abort_flag = 0;
-    ctl.kissued = ctl.vissued = ctl.qissued = 0;
+    ctl.qissued = 0;
+    for (int i = 0; i < CA_STAGES; ++i) ctl.last[i] = 0;
   }
   if (warp == 20) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -690,8 +738,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       CaItems items;
       CaItem it;
       uint32_t qph = 0, rph = 0;
-      int kst = 0, vst = 1;  // the stages of the next K and V tile, and their phases
-      uint32_t kph = 0, vph = 0;
+      CaPlace kt, vt;  // the next K and V tile
       // V: 64-value halves PT_HALF apart (leading offset), 8-token groups 1024
       // bytes apart
       const uint64_t q_desc = sw128_desc(q_s), k_desc = sw128_desc(ring);
@@ -702,12 +749,12 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       const bool lead = elect_one();
       while (ok && items.next(ctl, it, p.err)) {
         const bool two = it.two();
-        const int a = it.a, b = it.b, n0 = it.n0, stride = two ? 1 : 2;
+        const int a = it.a, b = it.b, n0 = it.n0, n = b - a, stride = two ? 1 : 2;
         // S_s = Q_s K^T with the K tile at the ring's next even position, by
         // the elected lane
         auto scores = [&](int s, bool last_use, bool last) {
           const uint64_t da = q_desc + (uint64_t)(two ? s * (PT_TILE >> 4) : 0);
-          const uint64_t db = k_desc + (uint64_t)(kst * (PT_TILE >> 4));
+          const uint64_t db = k_desc + (uint64_t)(kt.st * (PT_TILE >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t o = (uint64_t)(((k >> 2) * PT_HALF + (k & 3) * 32) >> 4);
@@ -715,20 +762,14 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           }
           tc_commit(sfull + 8 * s);
           if (last_use) {
-            tc_commit(empty0 + 8 * kst);
+            tc_commit(empty0 + 8 * kt.st);
             if (last) tc_commit(qempty);  // the query tiles' last use
           }
         };
-        auto next_k = [&]() {
-          kst += 2;
-          if (kst >= CA_STAGES) {
-            kst -= CA_STAGES;
-            kph ^= 1u;
-          }
-        };
+        vt.move(ca_first_v(two, n));
         ok = wait_all(qfull, qph, abort_flag, p.err);
         for (int i = 0; i < (two ? 1 : 2) && ok && a + i < b; ++i) {
-          ok = wait_all(full0 + 8 * kst, kph, abort_flag, p.err);
+          ok = wait_all(full0 + 8 * kt.st, kt.ph, abort_flag, p.err);
           tc_fence_after();
           if (ok && lead) {
             const bool last = a + i == b - 1;
@@ -736,15 +777,16 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             scores(two ? 1 : i, true, last);
           }
           __syncwarp();
-          next_k();
+          kt.move(ca_next_k(two, i, n));
         }
         // few instructions between the waits, and the tiles' waits ahead of
         // P's, which arrives last: this warp's latency is on every slot's path
         for (int j = a; j < b && ok; ++j) {
           const int jn = j + stride;
           const int s0 = two ? (j < n0 ? 0 : 1) : ((j - a) & 1), s1 = two ? 1 : s0;
-          ok = wait_all2(full0 + 8 * vst, vph, full0 + 8 * (jn < b ? kst : vst),
-                            jn < b ? kph : vph, abort_flag, p.err);
+          const bool k_now = two && jn < b;  // (one tile: its K tile comes after this V tile)
+          ok = wait_all2(full0 + 8 * vt.st, vt.ph, full0 + 8 * (k_now ? kt.st : vt.st),
+                         k_now ? kt.ph : vt.ph, abort_flag, p.err);
 #pragma unroll 1
           for (int s = s0; s <= s1 && ok; ++s) {
             const uint32_t ph = (rph >> s) & 1u;
@@ -752,7 +794,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             if (!ok) break;
             rph ^= 1u << s;
             tc_fence_after();
-            const uint64_t db = v_desc + (uint64_t)(vst * (PT_TILE >> 4));
+            const uint64_t db = v_desc + (uint64_t)(vt.st * (PT_TILE >> 4));
             if (lead) {
               const uint32_t began = j > a + (two ? 0 : s) ? 1u : 0u;
 #pragma unroll
@@ -768,18 +810,21 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
               for (int k = 4; k < 8; ++k)
                 ca_mma_ts(256 + s * 128, s * 128 + 32 + 8 * k, db + (uint64_t)((k * 2048) >> 4),
                           IDESC_O, 1u);
-              if (s == s1) tc_commit(empty0 + 8 * vst);
+              if (s == s1) tc_commit(empty0 + 8 * vt.st);
+            }
+            if (!two && jn < b) {
+              ok = wait_all(full0 + 8 * kt.st, kt.ph, abort_flag, p.err);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (lead) {
               if (jn < b && (!two || s == 1 || jn < n0)) scores(s, s == s1, jn == b - 1);
               else tc_commit(ofull + 8 * s);  // the slot's last product
             }
             __syncwarp();
           }
-          if (jn < b) next_k();
-          vst += 2;
-          if (vst >= CA_STAGES) {
-            vst -= CA_STAGES;
-            vph ^= 1u;
-          }
+          if (jn < b) kt.move(ca_next_k(two, jn - a, n));
+          vt.move(ca_next_v(two, j - a, n));
         }
         qph ^= 1u;
       }
@@ -794,45 +839,41 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       CaItem it;
       PagePieces pieces;
       const bool lead = elect_one();
-      uint32_t ph = 0;
-      int cnt = 0, st = 0;
+      CaPlace kt;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
         pieces.start(p.pages, it.seq, it.L, it.a, lane);
-        for (int j = it.a; j < it.b; ++j, ++cnt) {
+        for (int j = it.a; j < it.b; ++j) {
           const int page = pieces.take(p.pages);
-          ok = wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
+          ok = wait_all(empty0 + 8 * kt.st, kt.ph ^ 1u, abort_flag, p.err);
           if (!ok) break;
-          load_tile(p.pages, &k_map, ring + st * PT_TILE, full0 + 8 * st, page, pieces.slot, it.h,
-                       lead);
+          load_tile(p.pages, &k_map, ring + kt.st * PT_TILE, full0 + 8 * kt.st, page, pieces.slot,
+                    it.h, lead);
+          ctl.last[kt.st] = 2 + (int)kt.ph;
           pieces.step(p.pages);
-          st += 2;  // K tiles are the ring's even positions
-          if (st >= CA_STAGES) {
-            st -= CA_STAGES;
-            ph ^= 1u;
-          }
+          kt.move(ca_next_k(it.two(), j - it.a, it.b - it.a));
         }
       }
-      if (lane == 0) ctl.kissued = cnt;
     } else if (warp == 22) {
       // ------------------------------------------------------------------ V tiles
       CaItems items;
       CaItem it;
       PagePieces pieces;
       const bool lead = elect_one();
-      uint32_t vph = 0, ph = 0;
-      int cnt = 0, st = 1;
+      CaPlace vt;
+      uint32_t vph = 0;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
         pieces.start(p.pages, it.seq, it.L, it.a, lane);
-        for (int j = it.a; j < it.b; ++j, ++cnt) {
+        vt.move(ca_first_v(it.two(), it.b - it.a));
+        for (int j = it.a; j < it.b; ++j) {
           const int page = pieces.take(p.pages);
-          ok = wait_all(empty0 + 8 * st, ph ^ 1u, abort_flag, p.err);
+          ok = wait_all(empty0 + 8 * vt.st, vt.ph ^ 1u, abort_flag, p.err);
           if (!ok) break;
           const int nrow = it.L - j * CA_KT;  // the tile's rows that hold tokens
           const bool tail = nrow < CA_KT;
-          const uint32_t dst = ring + st * PT_TILE;
-          load_tile(p.pages, &v_map, dst, tail ? vraw : full0 + 8 * st, page, pieces.slot, it.h, lead);
+          const uint32_t dst = ring + vt.st * PT_TILE;
+          load_tile(p.pages, &v_map, dst, tail ? vraw : full0 + 8 * vt.st, page, pieces.slot, it.h, lead);
           pieces.step(p.pages);
           if (tail) {
             // (its own copies: waited for even after another role gave up)
@@ -850,16 +891,12 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
                              : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(full0 + 8 * st);
+            if (lane == 0) mbar_arrive(full0 + 8 * vt.st);
           }
-          st += 2;  // V tiles are the odd positions
-          if (st >= CA_STAGES) {
-            st -= CA_STAGES;
-            ph ^= 1u;
-          }
+          ctl.last[vt.st] = 2 + (int)vt.ph;
+          vt.move(ca_next_v(it.two(), j - it.a, it.b - it.a));
         }
       }
-      if (lane == 0) ctl.vissued = cnt;
     } else {
       // -------------------------------------- the items, ahead, and their Q tiles
       if (lane == 0) {
@@ -908,15 +945,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   pdl_trigger();
   if (ctl.abort_flag && threadIdx.x == 0) {
     // copies that were issued: each stage's last one, and the last query tiles
-    for (int back = 0; back < CA_STAGES; ++back) {
-      const int k = ctl.kissued - 1 - back, v = ctl.vissued - 1 - back;
-      if (k >= 0 && back <= CA_STAGES / 2)
-        mbar_wait(full0 + 8 * ((2 * k) % CA_STAGES), (uint32_t)((2 * k / CA_STAGES) & 1),
-                  abort_flag, p.err, TC_DRAIN_LIMIT, false);
-      if (v >= 0 && back <= CA_STAGES / 2)
-        mbar_wait(full0 + 8 * ((2 * v + 1) % CA_STAGES), (uint32_t)(((2 * v + 1) / CA_STAGES) & 1),
-                  abort_flag, p.err, TC_DRAIN_LIMIT, false);
-    }
+    for (int i = 0; i < CA_STAGES; ++i)
+      if (ctl.last[i])
+        mbar_wait(full0 + 8 * i, (uint32_t)ctl.last[i] & 1u, abort_flag, p.err, TC_DRAIN_LIMIT,
+                  false);
     if (ctl.qissued > 0)
       mbar_wait(qfull, (uint32_t)((ctl.qissued - 1) & 1), abort_flag, p.err, TC_DRAIN_LIMIT, false);
   }
@@ -946,11 +978,13 @@ __global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
   }
   const int4 gi = p.ginfo[2 * x];
   const int w = ca_weight(gi.z, p.TT);
-  const long long per = (long long)w * gi.w;
+  const int start = p.hdr[2];
+  const long long per = (long long)w * (gi.w + start);
   const int h = (int)((end - 1 - p.gpre[x]) / per);
   const long long u0 = p.gpre[x] + h * per;
   if (u0 < ca_bound(total, c0, n)) return;  // began in an earlier CTA
-  const int c1 = ca_owner(total, u0 + (long long)w * (gi.w - 1), n);
+  const int c1 =
+      gi.w == 1 ? c0 : ca_owner(total, u0 + (long long)w * (start + gi.w - 1), n);
   if (c1 == c0) return;
   const int rows = gi.z * p.G, per_tile = p.TT * p.G;
   for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += 8 * gridDim.y) {
