@@ -67,6 +67,9 @@ constexpr int CA_PLAN_THREADS = 1024;
 // 254 and 253 with 2, 3, 4 and 6. (With fewer, every CTA gets a step or two: a
 // single sequence's time is latency.)
 constexpr int CA_START = 3, CA_MANY = 16;
+// Chunk tokens that are loaded one by one into a tile that begins as zeros: MMA
+// rows of zeros draw less power than other tokens' (the part throttles at 1 kW)
+constexpr int CA_FEW = 4;
 constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sums
 
 struct CaArgs {
@@ -361,6 +364,7 @@ struct CaItems {
 
 __global__ void __launch_bounds__(CA_THREADS, 1)
     ca_attend_kernel(const __grid_constant__ CUtensorMap q_map,
+                     const __grid_constant__ CUtensorMap q1_map,
                      const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, const CaArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -414,6 +418,9 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  for (uint32_t i = threadIdx.x * 16; i < PT_TILE; i += CA_THREADS * 16)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(q_s + i), "r"(0) : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -927,11 +934,19 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           // (its K and V tiles are on their way already)
           if (at > 0 && !wait_bar(qempty, (uint32_t)(at - 1) & 1u, abort_flag, p.err)) break;
           const int tiles = w.w == 2 ? 2 : 1;
-          mbar_arrive_expect(qfull, (uint32_t)(tiles * 2 * p.TT * p.G * 128));
-          for (int s = 0; s < tiles; ++s)
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(q_s + s * PT_TILE + h * PT_HALF, &q_map, qfull, h * 64, w.h * p.G,
-                          w.gi.y + s * p.TT);
+          if (w.gi.z <= CA_FEW) {  // one by one: the tile's other rows stay zero
+            mbar_arrive_expect(qfull, (uint32_t)(w.gi.z * p.G * 256));
+            for (int i = 0; i < w.gi.z; ++i)
+              for (int h = 0; h < 2; ++h)
+                tma_load_3d(q_s + h * PT_HALF + i * p.G * 128, &q1_map, qfull, h * 64, w.h * p.G,
+                            w.gi.y + i);
+          } else {
+            mbar_arrive_expect(qfull, (uint32_t)(tiles * 2 * p.TT * p.G * 128));
+            for (int s = 0; s < tiles; ++s)
+              for (int h = 0; h < 2; ++h)
+                tma_load_3d(q_s + s * PT_TILE + h * PT_HALF, &q_map, qfull, h * 64, w.h * p.G,
+                            w.gi.y + s * p.TT);
+          }
           ctl.qissued = at + 1;
           more = w.next(false);
         }
@@ -1088,8 +1103,8 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   a.scale = d.scale;
   a.err = err;
 
-  CUtensorMap q_map, k_map, v_map;
-  if (!query_map(enc, &q_map, q, d, Nq, a.TT) ||
+  CUtensorMap q_map, q1_map, k_map, v_map;
+  if (!query_map(enc, &q_map, q, d, Nq, a.TT) || !query_map(enc, &q1_map, q, d, Nq, 1) ||
       !pool_map(enc, &k_map, c.k_pool, d, c, a.pages.box) ||
       !pool_map(enc, &v_map, c.v_pool, d, c, a.pages.box))
     return cudaErrorInvalidValue;
@@ -1097,7 +1112,8 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   if (e != cudaSuccess) return e;
   e = ensure_dynamic_smem(reinterpret_cast<const void *>(ca_attend_kernel), CA_SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(ca_attend_kernel, l.ctas, CA_THREADS, CA_SMEM, st, q_map, k_map, v_map, a);
+  e = launch_pdl(ca_attend_kernel, l.ctas, CA_THREADS, CA_SMEM, st, q_map, q1_map, k_map,
+                 v_map, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(ca_join_kernel, dim3(l.ctas, 12), 256, 0, st, a);
 }
