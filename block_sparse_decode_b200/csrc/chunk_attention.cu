@@ -74,7 +74,9 @@ constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sum
 
 struct CaArgs {
   const int32_t *seq_lens, *row_start;
-  int *hdr;          // [0] groups, [1] CTAs with work, [2] steps that an item's start counts as
+  int4 *first;       // [CTAs] {group, head, unit, end}: where a CTA's range begins (CaWalk); w < 0: empty
+  int4 *shared;      // [CTAs] {group, head, last CTA, -}: the item that goes on past it, or group -1
+  int *hdr;          // [0] steps that an item's start counts as
   long long *gpre;   // [Gmax + 1] prefix of the groups' units
   int4 *ginfo;       // [2 Gmax] {seq, first row, tokens, steps}, {tokens its first row sees, L, -, -}
   float *rec_lse;    // [CTAs][2][2][128]
@@ -109,11 +111,23 @@ __device__ long long ca_scan(long long v, long long *wsum, long long *total) {
   return off + x - v;
 }
 
+__device__ __forceinline__ long long ca_bound(long long total, int c, int n) {
+  return total * c / n;
+}
+// The CTA whose range holds a unit.
+__device__ __forceinline__ int ca_owner(long long total, long long unit, int n) {
+  int c = (int)(unit * n / total);
+  while (c + 1 < n && ca_bound(total, c + 1, n) <= unit) ++c;
+  while (c > 0 && ca_bound(total, c, n) > unit) --c;
+  return c;
+}
+
 // Units of one step: a step of two tiles counts twice that of one.
 __device__ __forceinline__ int ca_weight(int ntok, int TT) { return ntok > TT ? 2 : 1; }
 
 __global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int ctas) {
   __shared__ long long wsum[CA_PLAN_THREADS / 32];
+  __shared__ long long pre_s[CA_PLAN_THREADS + 1];  // the prefix, where it is short
   const int tid = threadIdx.x;
   pdl_wait();
   const int GT = 2 * a.TT;  // tokens of a group
@@ -170,31 +184,56 @@ __global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int 
     }
     long long tot;
     const long long off = tbase + ca_scan(n, wsum, &tot);
-    if (g < G) a.gpre[g] = off;
+    if (g < G) {
+      if (G <= CA_PLAN_THREADS) pre_s[g] = off;
+      else a.gpre[g] = off;
+    }
     tbase += tot;
   }
   if (tid == 0) {
-    a.gpre[G] = tbase;
-    a.hdr[0] = G;
-    // every range is at least as long as the units between two steps, so every
-    // CTA inside an item's range has a step of it
-    a.hdr[1] = (int)min((long long)ctas, max(1LL, tbase / (2 * (start + 1))));
-    a.hdr[2] = start;
+    (G <= CA_PLAN_THREADS ? pre_s : a.gpre)[G] = tbase;
+    a.hdr[0] = start;
+  }
+  __syncthreads();
+  // where every CTA's range begins, and the items that CTAs share. Every range
+  // is at least as long as the units between two steps, so every CTA inside an
+  // item's range has a step of it
+  const long long *pre = G <= CA_PLAN_THREADS ? pre_s : a.gpre, total = tbase;
+  const int n = (int)min((long long)ctas, max(1LL, total / (2 * (start + 1))));
+  for (int c = tid; c < ctas; c += CA_PLAN_THREADS) {
+    int4 f = make_int4(0, 0, 0, -1), e = make_int4(-1, 0, 0, 0);
+    if (total > 0 && c < n) {
+      const long long lo = ca_bound(total, c, n), hi = ca_bound(total, c + 1, n);
+      auto find = [&](long long unit, int4 &gi, int &h, long long &u0) {
+        int x = 0, y = G - 1;  // the last group that starts at or before the unit
+        while (x < y) {
+          const int m = (x + y + 1) >> 1;
+          if (pre[m] <= unit) x = m; else y = m - 1;
+        }
+        gi = a.ginfo[2 * x];
+        const long long per = (long long)ca_weight(gi.z, a.TT) * (gi.w + start);
+        h = (int)((unit - pre[x]) / per);
+        u0 = pre[x] + h * per;
+        return x;
+      };
+      int4 gi;
+      int h;
+      long long u0;
+      int g = find(lo, gi, h, u0);
+      f = make_int4(g, h, (int)(u0 - lo), (int)(hi - lo));
+      g = find(hi - 1, gi, h, u0);
+      if (u0 >= lo && gi.w > 1) {  // began here
+        const int w = ca_weight(gi.z, a.TT);
+        const int last = ca_owner(total, u0 + (long long)w * (start + gi.w - 1), n);
+        if (last > c) e = make_int4(g, h, last, 0);
+      }
+    }
+    a.first[c] = f;
+    a.shared[c] = e;
   }
 }
 
 // ------------------------------------------------------------------ items
-
-__device__ __forceinline__ long long ca_bound(long long total, int c, int n) {
-  return total * c / n;
-}
-// The CTA whose range holds a unit.
-__device__ __forceinline__ int ca_owner(long long total, long long unit, int n) {
-  int c = (int)(unit * n / total);
-  while (c + 1 < n && ca_bound(total, c + 1, n) <= unit) ++c;
-  while (c > 0 && ca_bound(total, c, n) > unit) --c;
-  return c;
-}
 
 // The items of one CTA's range, in order. An item of n steps has w (start + n)
 // units: with many steps in all, an item's start (queries, first tiles, its
@@ -209,23 +248,14 @@ struct CaWalk {
   const CaArgs &p;
 
   __device__ CaWalk(const CaArgs &args, int c) : p(args) {
-    const int n = p.hdr[1], G = p.hdr[0];
-    u = hi = g = h = start = 0;
+    const int4 f = p.first[c];
+    start = p.hdr[0];
+    g = f.x;
+    h = f.y;
+    u = f.z;
+    hi = f.w;
     w = 1;
-    if (G == 0 || c >= n) return;
-    start = p.hdr[2];
-    const long long total = p.gpre[G], lo = ca_bound(total, c, n);
-    hi = (int)(ca_bound(total, c + 1, n) - lo);
-    int x = 0, y = G - 1;  // last group that starts at or before lo
-    while (x < y) {
-      const int m = (x + y + 1) >> 1;
-      if (p.gpre[m] <= lo) x = m; else y = m - 1;
-    }
-    g = x;
-    load();
-    const long long u0 = p.gpre[g], per = (long long)w * (gi.w + start);
-    h = (int)((lo - u0) / per);
-    u = (int)(u0 + h * per - lo);
+    if (hi > 0) load();
   }
   __device__ void load() {
     gi = p.ginfo[2 * g];
@@ -982,25 +1012,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
 __global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
   pdl_wait();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
-  const int G = p.hdr[0], n = p.hdr[1];
-  if (G == 0 || c0 + 1 >= n) return;
-  const long long total = p.gpre[G];
-  const long long end = ca_bound(total, c0 + 1, n);
-  int x = 0, y = G - 1;  // the group that holds the unit before the range's end
-  while (x < y) {
-    const int m = (x + y + 1) >> 1;
-    if (p.gpre[m] <= end - 1) x = m; else y = m - 1;
-  }
-  const int4 gi = p.ginfo[2 * x];
-  const int w = ca_weight(gi.z, p.TT);
-  const int start = p.hdr[2];
-  const long long per = (long long)w * (gi.w + start);
-  const int h = (int)((end - 1 - p.gpre[x]) / per);
-  const long long u0 = p.gpre[x] + h * per;
-  if (u0 < ca_bound(total, c0, n)) return;  // began in an earlier CTA
-  const int c1 =
-      gi.w == 1 ? c0 : ca_owner(total, u0 + (long long)w * (start + gi.w - 1), n);
-  if (c1 == c0) return;
+  const int4 e = p.shared[c0];
+  if (e.x < 0) return;
+  const int4 gi = p.ginfo[2 * e.x];
+  const int h = e.y, c1 = e.z;
   const int rows = gi.z * p.G, per_tile = p.TT * p.G;
   for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += 8 * gridDim.y) {
     const int at = i < per_tile ? i : 128 + i - per_tile;
@@ -1047,7 +1062,7 @@ __global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
 // ------------------------------------------------------------------ host
 
 struct CaLayout {
-  size_t gpre, ginfo, lse, o, bytes;
+  size_t first, shared, gpre, ginfo, lse, o, bytes;
   int Gmax, TT, ctas;
 };
 
@@ -1057,7 +1072,9 @@ CaLayout ca_layout(const qsa_dims &d, int S, int Nq) {
   l.Gmax = S + Nq / (2 * l.TT);
   l.ctas = device_sm_count();
   auto r = [](size_t x) { return (x + 255) / 256 * 256; };
-  l.gpre = 256;
+  l.first = 256;
+  l.shared = l.first + r(16 * (size_t)l.ctas);
+  l.gpre = l.shared + r(16 * (size_t)l.ctas);
   l.ginfo = l.gpre + r(8 * ((size_t)l.Gmax + 1));
   l.lse = l.ginfo + r(32 * (size_t)l.Gmax);
   l.o = l.lse + r((size_t)l.ctas * 512 * 4);
@@ -1085,6 +1102,8 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   a.seq_lens = seq_lens;
   a.row_start = row_start;
   a.hdr = reinterpret_cast<int *>(w);
+  a.first = reinterpret_cast<int4 *>(w + l.first);
+  a.shared = reinterpret_cast<int4 *>(w + l.shared);
   a.gpre = reinterpret_cast<long long *>(w + l.gpre);
   a.ginfo = reinterpret_cast<int4 *>(w + l.ginfo);
   a.rec_lse = reinterpret_cast<float *>(w + l.lse);

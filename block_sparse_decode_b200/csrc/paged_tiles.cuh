@@ -68,6 +68,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         : "r"(bar), "r"(parity), "r"(PT_WAIT_NS)
         : "memory");
     if (done) return true;
+    __nanosleep(20);  // (polling slows the warps that compute: ragged chunks 237 us without)
     if (*abort_flag) return false;
   }
   *abort_flag = 1;
