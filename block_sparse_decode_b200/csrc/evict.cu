@@ -19,6 +19,7 @@ namespace {
 constexpr int EV_THREADS = 1024;
 constexpr int EV_WARPS = EV_THREADS / 32;
 constexpr int EV_BINS = 2048;
+constexpr int EV_CACHED = 50 * 1024;  // weights: 200 KB, 204,800 tokens
 
 struct EvictArgs {
   const int32_t *seq_lens, *table, *dst;
@@ -27,6 +28,7 @@ struct EvictArgs {
   int32_t *kept, *new_lens;
   uint4 *k_pool, *v_pool, *x_pool, *side_pool;
   int ld, keep, sink, recent;
+  int cached;  // weights that fit the select kernel's shared memory
   int P, max_pages, num_pages;
   int kv_vec, x_vec;  // 16-byte vectors per token row of K (= of V), per indexer key
   unsigned *err;
@@ -40,15 +42,31 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+constexpr int EV_BATCH = 8;  // weights that a thread requests together
+
+// Sum of the values of the warps before this one (v: this warp's, the same in
+// every lane). wsum: one value per warp; barriers included.
+__device__ __forceinline__ int before_warp(int v, int *wsum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) wsum[warp] = v;
+  __syncthreads();
+  int x = lane < warp ? wsum[lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  return x;
+}
+
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
+  extern __shared__ float cache[];
   __shared__ int hist[EV_BINS];
-  __shared__ int wsum[EV_WARPS], wsum2[EV_WARPS];
+  __shared__ int wsum[EV_WARPS];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   const int L = a.seq_lens[b];
-  const float *mass = a.mass + (size_t)b * a.ld;
+  const float *row = a.mass + (size_t)b * a.ld;
   float *mass_out = a.mass_out + (size_t)b * a.ld;
   int32_t *kept = a.kept + (size_t)b * a.keep;
   const bool bad = L < 0 || (long long)L > 4LL * a.ld;
@@ -61,9 +79,24 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
   if (n == nb) {
     for (int i = tid; i < n; i += EV_THREADS) {
       kept[i] = i;
-      mass_out[i] = mass[i];
+      mass_out[i] = row[i];
     }
     return;
+  }
+  // the weights are read five times: from shared memory where they fit
+  const float *mass = row;
+  if (nb <= a.cached) {
+    for (int j0 = tid; j0 < nb; j0 += EV_THREADS * EV_BATCH) {
+      float m[EV_BATCH];
+#pragma unroll
+      for (int u = 0; u < EV_BATCH; ++u)
+        if (j0 + u * EV_THREADS < nb) m[u] = row[j0 + u * EV_THREADS];
+#pragma unroll
+      for (int u = 0; u < EV_BATCH; ++u)
+        if (j0 + u * EV_THREADS < nb) cache[j0 + u * EV_THREADS] = m[u];
+    }
+    __syncthreads();
+    mass = cache;
   }
   // candidates: [sink, nb - recent); `need` of them stay
   const int c0 = a.sink, c1 = nb - a.recent;
@@ -75,16 +108,27 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
     const int sh = shifts[r], bins = 1 << widths[r];
     for (int i = tid; i < bins; i += EV_THREADS) hist[i] = 0;
     __syncthreads();
-    for (int j0 = c0; j0 < c1; j0 += EV_THREADS) {
-      const int j = j0 + tid;
-      int bin = -1;
-      if (j < c1) {
-        const uint32_t key = mass_key(mass[j]);
-        if ((key & mask) == prefix) bin = (int)((key >> sh) & (uint32_t)(bins - 1));
+    for (int j0 = c0; j0 < c1; j0 += EV_THREADS * EV_BATCH) {
+      float m[EV_BATCH];
+#pragma unroll
+      for (int u = 0; u < EV_BATCH; ++u) {
+        const int j = j0 + u * EV_THREADS + tid;
+        m[u] = j < c1 ? mass[j] : 0.f;
       }
-      // equal bins of a warp are counted with one add
-      const unsigned same = __match_any_sync(0xffffffffu, bin);
-      if (bin >= 0 && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+#pragma unroll
+      for (int u = 0; u < EV_BATCH; ++u) {
+        if (j0 + u * EV_THREADS >= c1) break;
+        int bin = -1;
+        const uint32_t key = mass_key(m[u]);
+        if (j0 + u * EV_THREADS + tid < c1 && (key & mask) == prefix)
+          bin = (int)((key >> sh) & (uint32_t)(bins - 1));
+        // (32 equal weights are one add; otherwise few lanes meet in a bin)
+        if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
+          if (bin >= 0 && lane == 0) atomicAdd(&hist[bin], 32);
+        } else if (bin >= 0) {
+          atomicAdd(&hist[bin], 1);
+        }
+      }
     }
     __syncthreads();
     // from the top bin down: the bin in which the need-th largest lies
@@ -102,10 +146,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    int before = x - tot;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
+    int before = x - tot + before_warp(__shfl_sync(0xffffffffu, x, 31), wsum);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       if (before < need && before + mine[u] >= need) {
@@ -126,44 +167,53 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(EvictArgs a) {
   const int per = ((nb + EV_WARPS - 1) / EV_WARPS + 31) / 32 * 32;
   const int j0 = warp * per, j1 = min(nb, j0 + per);
   int gt = 0, eq = 0;
-  for (int j = j0 + lane; j < j1; j += 32) {
-    const bool always = j < c0 || j >= c1;
-    const uint32_t key = always ? 0u : mass_key(mass[j]);
-    gt += always || key > cut;
-    eq += !always && key == cut;
+  for (int jb = j0; jb < j1; jb += 32 * EV_BATCH) {
+    float m[EV_BATCH];
+#pragma unroll
+    for (int u = 0; u < EV_BATCH; ++u) {
+      const int j = jb + 32 * u + lane;
+      m[u] = j < j1 ? mass[j] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < EV_BATCH; ++u) {
+      const int j = jb + 32 * u + lane;
+      const bool in = j < j1, always = in && (j < c0 || j >= c1);
+      const uint32_t key = mass_key(m[u]);
+      gt += always || (in && key > cut);
+      eq += in && !always && key == cut;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     gt += __shfl_xor_sync(0xffffffffu, gt, o);
     eq += __shfl_xor_sync(0xffffffffu, eq, o);
   }
-  if (lane == 0) {
-    wsum[warp] = gt;
-    wsum2[warp] = eq;
-  }
-  __syncthreads();
-  int gb = 0, eb = 0;
-  for (int w = 0; w < warp; ++w) {
-    gb += wsum[w];
-    eb += wsum2[w];
-  }
+  int gb = before_warp(gt, wsum), eb = before_warp(eq, wsum);
   const unsigned below = (1u << lane) - 1u;
-  for (int j = j0; j < j1; j += 32) {
-    const int jj = j + lane;
-    const bool in = jj < j1;
-    const bool always = in && (jj < c0 || jj >= c1);
-    const float m = in ? mass[jj] : 0.f;
-    const uint32_t key = in && !always ? mass_key(m) : 0u;
-    const bool g = always || (in && key > cut), e = in && !always && key == cut;
-    const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-    const int er = eb + __popc(be & below);  // equal ones before this block
-    if (g || (e && er < need)) {
-      const int at = gb + __popc(bg & below) + min(er, need);
-      kept[at] = jj;
-      mass_out[at] = m;
+  for (int jb = j0; jb < j1; jb += 32 * EV_BATCH) {
+    float m[EV_BATCH];
+#pragma unroll
+    for (int u = 0; u < EV_BATCH; ++u) {
+      const int j = jb + 32 * u + lane;
+      m[u] = j < j1 ? mass[j] : 0.f;
     }
-    gb += __popc(bg);
-    eb += __popc(be);
+#pragma unroll
+    for (int u = 0; u < EV_BATCH; ++u) {
+      const int j = jb + 32 * u + lane;
+      if (jb + 32 * u >= j1) break;
+      const bool in = j < j1, always = in && (j < c0 || j >= c1);
+      const uint32_t key = mass_key(m[u]);
+      const bool g = always || (in && key > cut), e = in && !always && key == cut;
+      const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+      const int er = eb + __popc(be & below);  // equal ones before this block
+      if (g || (e && er < need)) {
+        const int at = gb + __popc(bg & below) + min(er, need);
+        kept[at] = j;
+        mass_out[at] = m[u];
+      }
+      gb += __popc(bg);
+      eb += __popc(be);
+    }
   }
 }
 
@@ -183,16 +233,25 @@ __device__ __forceinline__ int block_page(const EvictArgs &a, const int32_t *row
   return page;
 }
 
-__device__ __forceinline__ void copy_vecs(uint4 *dst, const uint4 *src, int n, int lane) {
+// n vectors from each of two rows of sources, all of a round requested before
+// the first is written.
+__device__ __forceinline__ void copy_vecs(uint4 *d0, const uint4 *s0, uint4 *d1, const uint4 *s1,
+                                          int n, int lane) {
   constexpr int U = 8;
-  for (int i0 = 0; i0 < n; i0 += 32 * U) {
-    uint4 v[U];
+  for (int i0 = lane; i0 < n; i0 += 32 * U) {
+    uint4 v[U], w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + 32 * u + lane < n) v[u] = src[i0 + 32 * u + lane];
+      if (i0 + 32 * u < n) {
+        v[u] = s0[i0 + 32 * u];
+        w[u] = s1[i0 + 32 * u];
+      }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + 32 * u + lane < n) dst[i0 + 32 * u + lane] = v[u];
+      if (i0 + 32 * u < n) {
+        d0[i0 + 32 * u] = v[u];
+        d1[i0 + 32 * u] = w[u];
+      }
   }
 }
 
@@ -209,11 +268,20 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(EvictArgs a) {
   if (sp < 0 || dp < 0) return;
   const int rpp = a.P / 4;
   const size_t s = (size_t)sp * rpp + blk % rpp, d = (size_t)dp * rpp + i % rpp;
-  copy_vecs(a.k_pool + d * 4 * a.kv_vec, a.k_pool + s * 4 * a.kv_vec, toks * a.kv_vec, lane);
-  copy_vecs(a.v_pool + d * 4 * a.kv_vec, a.v_pool + s * 4 * a.kv_vec, toks * a.kv_vec, lane);
-  copy_vecs(a.x_pool + d * 4 * a.x_vec, a.x_pool + s * 4 * a.x_vec, toks * a.x_vec, lane);
-  if (toks == 4)
-    copy_vecs(a.side_pool + d * a.x_vec, a.side_pool + s * a.x_vec, a.x_vec, lane);
+  // (the small rows first: their loads overlap with the large ones')
+  uint4 x[2], y;
+  const int xn = toks * a.x_vec;  // at most 64
+  const uint4 *xs = a.x_pool + s * 4 * a.x_vec;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (lane + 32 * u < xn) x[u] = xs[lane + 32 * u];
+  if (toks == 4 && lane < a.x_vec) y = a.side_pool[s * a.x_vec + lane];
+  copy_vecs(a.k_pool + d * 4 * a.kv_vec, a.k_pool + s * 4 * a.kv_vec,
+            a.v_pool + d * 4 * a.kv_vec, a.v_pool + s * 4 * a.kv_vec, toks * a.kv_vec, lane);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (lane + 32 * u < xn) a.x_pool[d * 4 * a.x_vec + lane + 32 * u] = x[u];
+  if (toks == 4 && lane < a.x_vec) a.side_pool[d * a.x_vec + lane] = y;
 }
 
 }  // namespace
@@ -244,7 +312,11 @@ cudaError_t launch_evict(const qsa_dims &d, const qsa_cache &c, int B, const int
   a.kv_vec = d.Hkv * d.D / 8;
   a.x_vec = d.di / 8;
   a.err = err;
-  cudaError_t e = launch_pdl(evict_select_kernel, B, EV_THREADS, 0, st, a);
+  a.cached = std::min(ld, EV_CACHED);
+  const size_t smem = (size_t)a.cached * sizeof(float);
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(evict_select_kernel), smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(evict_select_kernel, B, EV_THREADS, smem, st, a);
   if (e != cudaSuccess) return e;
   const int most = std::min(keep, ld);
   return launch_pdl(evict_copy_kernel, dim3((most + 7) / 8, B), 256, 0, st, a);
