@@ -24,8 +24,8 @@
 // warps work on its softmax, the tensor cores work for the other.
 //   warps 0-7, 8-15 softmax of slot 0, 1: a thread holds half a row of S (two
 //                   warps hold a row's halves, and exchange its maximum)
-//   warps 16-19     rescale O where a maximum grew; at an item's end read O
-//                   and write the result
+//                   At an item's end each writes half of the rows' results
+//   warps 16-19     rescale O where a maximum grew
 //   warp 20         issues the MMAs
 //   warp 21, 22     TMA of K tiles; of V tiles, whose rows past L_s are set to
 //                   zero (0 * NaN in a stale slot would reach the sum)
@@ -305,7 +305,7 @@ __device__ __forceinline__ bool ca_active(int s, int j, int a, int n0) {
 struct CaCtrl {
   uint64_t full[CA_STAGES], empty[CA_STAGES];
   uint64_t qfull, qempty, vraw, drain;
-  uint64_t sfull[2], ready[2], ready2[2], corr[2], ofull[2], fread[2];
+  uint64_t sfull[2], ready[2], ready2[2], corr[2], ofull[2], fin, fread;
   uint64_t ifull[CA_ITEMS], iempty[CA_ITEMS];
   CaItem item[CA_ITEMS];
   uint32_t tmem;
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
   const uint32_t qfull = smem_u32(&ctl.qfull), qempty = smem_u32(&ctl.qempty);
   const uint32_t vraw = smem_u32(&ctl.vraw), drain = smem_u32(&ctl.drain);
   const uint32_t sfull = smem_u32(&ctl.sfull[0]), ready = smem_u32(&ctl.ready[0]);
-  const uint32_t ready2 = smem_u32(&ctl.ready2[0]), fread = smem_u32(&ctl.fread[0]);
+  const uint32_t ready2 = smem_u32(&ctl.ready2[0]), fread = smem_u32(&ctl.fread);
+  const uint32_t fin = smem_u32(&ctl.fin);
   const uint32_t corr = smem_u32(&ctl.corr[0]), ofull = smem_u32(&ctl.ofull[0]);
 
   if (threadIdx.x == 0) {
@@ -424,6 +425,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     mbar_init(qempty, 1);
     mbar_init(vraw, 1);
     mbar_init(drain, 1);
+    mbar_init(fin, 4);
+    mbar_init(fread, 8);
     for (int i = 0; i < CA_ITEMS; ++i) {
       mbar_init(smem_u32(&ctl.ifull[i]), 1);
       mbar_init(smem_u32(&ctl.iempty[i]), CA_READERS);
@@ -434,7 +437,6 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       mbar_init(ready2 + 8 * s, 4);
       mbar_init(corr + 8 * s, 4);
       mbar_init(ofull + 8 * s, 1);
-      mbar_init(fread + 8 * s, 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ctl.abort_flag = 0;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     const uint32_t done = (half == 0 ? ready : ready2) + 8 * s;  // this half of P is written
     const int pair = 1 + s * 4 + (warp & 3);  // barrier of the two warps of these rows
     uint32_t sph = 0, fph = 0, oph = 0;
-    bool ended = false;  // an item's end that the correction warps have to read first
+    bool ended = false;  // slot 1's part of a one-tile item, which slot 0 has to read first
     // The two warps stop together: every wait that may give up is followed by
     // their barrier, which combines the outcomes.
     auto both = [&](bool ok) {
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       for (int j = it.a; j < it.b; ++j) {
         if (!ca_active(s, j, it.a, n0)) continue;
         if (ended) {
-          ok = wait_all(fread + 8 * s, fph, abort_flag, p.err);
+          ok = wait_all(fread, fph, abort_flag, p.err);
           fph ^= 1u;
           ended = false;
         }
@@ -602,29 +604,104 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         any = true;
       }
       if (!ok) break;
-      if (any) {  // the item's sum and maximum, for its end
-        both(true);
-        if (half == 1) ctl.pm[s][1][r] = l;
-        both(true);
+      const size_t rec =
+          ((size_t)blockIdx.x * 2 + (it.a == 0 ? 1 : 0)) * 256 + s * 128 + r;
+      if (!any) {  // slot 0's rows see none of this CTA's steps of a two-tile item
+        if (it.two() && valid && half == 0) p.rec_lse[rec] = -INFINITY;
+        continue;
+      }
+      // the item's end: the row's sum over both halves, then this half of the
+      // result's columns, once the slot's last product is in
+      ctl.pm[s][half][r] = l;
+      both(true);
+      l += ctl.pm[s][half ^ 1][r];
+      ok = wait_all(ofull + 8 * s, oph, abort_flag, p.err);
+      oph ^= 1u;
+      tc_fence_after();
+      const bool two = it.two();
+      if (!two && s == 1) {  // one tile: slot 0 writes the result of both
+        both(true);  // (the sums have been read)
         if (half == 0) {
-          // (the last product had the correction warps' arrival: they have
-          // seen the last rescaling)
-          ok = wait_all(ofull + 8 * s, oph, abort_flag, p.err);
-          oph ^= 1u;
-          ctl.pm[s][0][r] = l + ctl.pm[s][1][r];
-          ctl.pm[s][1][r] = m;
+          ctl.pm[1][0][r] = l;
+          ctl.pm[1][1][r] = m;
           __syncwarp();
-          if (lane == 0) mbar_arrive(corr + 8 * s);
+          if (lane == 0) mbar_arrive(fin);
         }
         ended = true;
+        continue;
       }
+      const bool has1 = !two && it.b - it.a > 1;  // slot 1 has a part
+      float l1 = 0.f, m1 = -INFINITY;
+      if (has1) {
+        ok = ok && wait_all(fin, fph, abort_flag, p.err);
+        fph ^= 1u;
+        tc_fence_after();
+        l1 = ctl.pm[1][0][r];
+        m1 = ctl.pm[1][1][r];
+      }
+      if (ok && live) {
+        const float M = fmaxf(l > 0.f ? m : -INFINITY, l1 > 0.f ? m1 : -INFINITY);
+        const float e0 = l > 0.f ? ex2_approx(m - M) : 0.f;
+        const float e1 = l1 > 0.f ? ex2_approx(m1 - M) : 0.f;
+        const float sum = e0 * l + e1 * l1;
+        const float f0 = sum > 0.f ? e0 / sum : 0.f, f1 = sum > 0.f ? e1 / sum : 0.f;
+        const bool whole = it.whole != 0;
+        const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
+        if (valid && half == 0) {
+          const float lse = sum > 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          if (!whole) p.rec_lse[rec] = lse;
+          else if (p.lse != nullptr) p.lse[row] = lse;
+        }
+        const uint32_t to =
+            tmem + (uint32_t)(256 + s * 128 + half * 64) + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          float o[32];
+          tc_ld32_nowait(to + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
+          if (has1) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 16) {
+              float o1[16];
+              tc_ld16(to + 128 + 32 * c + k, o1);
+              if (f1 > 0.f) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[k + i] = fmaf(o1[i], f1, o[k + i]);
+              }
+            }
+          }
+          if (!valid) continue;
+          const int col = half * 64 + 32 * c;
+          if (whole && p.out_bf16) {
+            uint4 *d =
+                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              d[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                                pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                                pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+          } else {
+            float4 *d = reinterpret_cast<float4 *>(
+                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (has1 && lane == 0) mbar_arrive(fread);
     }
   } else if (warp < 20) {
-    // ------------------------------------------------- correction and results
+    // ------------------------------------------------------------- correction
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int r = (warp & 3) * 32 + lane;
     const uint32_t to = tmem + 256u + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t cph = 0, oph = 0;  // a bit per slot
+    uint32_t cph = 0, rph = 0, began = 0;  // a bit per slot
     CaItems items;
     CaItem it;
     bool ok = true;
@@ -659,110 +736,18 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
               }
               ca_wait_st();
             }
+          } else if ((began >> s) & 1u) {
+            // an item's first step has nothing to rescale; but the step before
+            // it has to be complete before this one's arrival counts
+            ok = wait_all(ready + 8 * s, ((rph >> s) & 1u) ^ 1u, abort_flag, p.err);
+            if (!ok) continue;
           }
           any |= 1u << s;
+          began |= 1u << s;
+          rph ^= 1u << s;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(ready + 8 * s);
-        }
-      }
-      if (!ok) break;
-      // the end of the item: wait for its last products and sums
-      float l[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!((any >> s) & 1u) || !ok) continue;
-        ok = wait_all2(corr + 8 * s, (cph >> s) & 1u, ofull + 8 * s, (oph >> s) & 1u, abort_flag,
-                       p.err);
-        cph ^= 1u << s;
-        oph ^= 1u << s;
-        if (!ok) continue;
-        l[s] = ctl.pm[s][0][r];
-        m[s] = ctl.pm[s][1][r];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(fread + 8 * s);
-      }
-      if (!ok) break;
-      tc_fence_after();
-      const bool whole = it.whole != 0;
-      const int piece = it.a == 0 ? 1 : 0;  // record of a partial result
-      const bool two = it.two();
-#pragma unroll 1
-      for (int s = 0; s < (two ? 2 : 1); ++s) {
-        const int tok = s * p.TT + r / p.G;
-        const bool valid = r < p.TT * p.G && tok < it.ntok;
-        if (!__any_sync(0xffffffffu, valid)) continue;
-        // weights of the slot's O (two tiles), or of both slots' (one tile)
-        float f0 = 0.f, f1 = 0.f, lse = -INFINITY;
-        if (two) {
-          const float ls = s == 0 ? l[0] : l[1], ms = s == 0 ? m[0] : m[1];
-          if (ls > 0.f) {
-            f0 = 1.f / ls;
-            lse = (ms + log2f(ls)) * 0.6931471805599453f;
-          }
-        } else {
-          const float M = fmaxf(l[0] > 0.f ? m[0] : -INFINITY, l[1] > 0.f ? m[1] : -INFINITY);
-          const float e0 = l[0] > 0.f ? ex2_approx(m[0] - M) : 0.f;
-          const float e1 = l[1] > 0.f ? ex2_approx(m[1] - M) : 0.f;
-          const float sum = e0 * l[0] + e1 * l[1];
-          if (sum > 0.f) {
-            f0 = e0 / sum;
-            f1 = e1 / sum;
-            lse = (M + log2f(sum)) * 0.6931471805599453f;
-          }
-        }
-        const bool has = !two || ((any >> s) & 1u);
-        const bool has1 = !two && (any & 2u);
-        const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
-        const size_t rec = ((size_t)blockIdx.x * 2 + piece) * 256 + s * 128 + r;
-        if (valid) {
-          if (!whole) p.rec_lse[rec] = lse;
-          else if (p.lse != nullptr) p.lse[row] = lse;
-        }
-        if (!has) continue;
-        const uint32_t ta = to + (two ? s * 128 : 0);
-        auto put = [&](const float *o, int col, int n) {  // n values from column col on
-          if (!valid) return;
-          if (whole && p.out_bf16) {
-            uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D +
-                                                 col);
-#pragma unroll
-            for (int i = 0; i < n / 8; ++i)
-              d[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
-                                pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
-                                pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-          } else {
-            float4 *d = reinterpret_cast<float4 *>(
-                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + col);
-#pragma unroll
-            for (int i = 0; i < n / 4; ++i)
-              d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-        };
-        if (!has1) {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tc_ld32_nowait(ta + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
-            put(o, 32 * c, 32);
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            float o[16], o1[16];
-            tc_ld16(ta + 16 * c, o);
-            tc_ld16(to + 128 + 16 * c, o1);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
-              if (f1 > 0.f) o[i] = fmaf(o1[i], f1, o[i]);
-            }
-            put(o, 16 * c, 16);
-          }
         }
       }
     }
