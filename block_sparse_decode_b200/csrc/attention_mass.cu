@@ -76,7 +76,7 @@ __device__ __forceinline__ bool am_chunk(const AmArgs &a, int s, int &r0, int &T
   const int r1 = a.row_start[s + 1];
   L = a.seq_lens[s];
   T = r1 - r0;
-  return !(r0 < 0 || r1 < r0 || r1 > a.Nq || T > L ||
+  return !(r0 < 0 || r1 < r0 || r1 > a.Nq || T > L || L > PT_MAX_LEN ||
            (long long)L > (long long)a.pages.max_pages * a.pages.P || (long long)L > 4LL * a.ld);
 }
 // First query block of a chunk that sees any token of item u.
@@ -189,25 +189,25 @@ __device__ long long am_find(const AmArgs &p, long long at, AmItem &it) {
 
 // ------------------------------------------------------------------ weigh
 
-// 2^x of a pair on the fp32 units, for x < 128: x = n + f with n the nearest
-// whole number (left in the low bits of x + 1.5 * 2^23) and |f| <= 1/2, 2^f by
-// the degree-5 polynomial of least relative error there (Remez exchange; 2.4e-7
-// with its fp32 roundings), and n added to its exponent. x below -126 counts
-// as -126: its weight, at most 2^-126, is 0 instead of that.
+// 2^x of a pair on the fp32 units: x = n + f with n the nearest whole number
+// (left in the low bits of x + 1.5 * 2^23) and |f| <= 1/2, 2^f by the polynomial
+// 1 + f (c1 + ... c5 f^4) of least relative error there (a linear program on a
+// grid; 1.7e-7 with its fp32 roundings), and n added to its exponent. x below
+// -127 counts as -127, whose 2^x is then exactly 0; x above 127 counts as 127.
 __device__ __forceinline__ unsigned long long exp2_poly(unsigned long long x) {
   float x0, x1;
   f2_unpack(x, x0, x1);
-  const float m0 = fmaxf(x0, -126.f), m1 = fmaxf(x1, -126.f);
+  const float m0 = fminf(fmaxf(x0, -127.f), 127.f), m1 = fminf(fmaxf(x1, -127.f), 127.f);
   const unsigned long long m = f2_pack(m0, m1);
   const unsigned long long r = f2_add(m, f2_pack(12582912.f, 12582912.f));
   const unsigned long long f =
       f2_fma(f2_add(r, f2_pack(-12582912.f, -12582912.f)), f2_pack(-1.f, -1.f), m);
-  unsigned long long y = f2_fma(f, f2_pack(0x1.5c08e6p-10f, 0x1.5c08e6p-10f),
-                                f2_pack(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
-  y = f2_fma(f, y, f2_pack(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
-  y = f2_fma(f, y, f2_pack(0x1.ebf918p-3f, 0x1.ebf918p-3f));
-  y = f2_fma(f, y, f2_pack(0x1.62e428p-1f, 0x1.62e428p-1f));
-  y = f2_fma(f, y, f2_pack(0x1.000002p+0f, 0x1.000002p+0f));
+  unsigned long long y = f2_fma(f, f2_pack(0x1.5bba0cp-10f, 0x1.5bba0cp-10f),
+                                f2_pack(0x1.3cea88p-7f, 0x1.3cea88p-7f));
+  y = f2_fma(f, y, f2_pack(0x1.c6b754p-5f, 0x1.c6b754p-5f));
+  y = f2_fma(f, y, f2_pack(0x1.ebf9bcp-3f, 0x1.ebf9bcp-3f));
+  y = f2_fma(f, y, f2_pack(0x1.62e42ap-1f, 0x1.62e42ap-1f));
+  y = f2_fma(f, y, f2_pack(1.f, 1.f));
   float r0, r1, y0, y1;
   f2_unpack(r, r0, r1);
   f2_unpack(y, y0, y1);

@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int 
       const int r1 = a.row_start[s + 1];
       L = a.seq_lens[s];
       T = r1 - r0;
-      if (r0 < 0 || r1 < r0 || r1 > a.Nq || T > L || (long long)L > (long long)a.pages.max_pages * a.pages.P)
+      if (r0 < 0 || r1 < r0 || r1 > a.Nq || T > L || L > PT_MAX_LEN ||
+          (long long)L > (long long)a.pages.max_pages * a.pages.P)
         raise_err(a.err, ERR_LEN);
       else
         ng = (T + GT - 1) / GT;
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
     const uint32_t ts =
         tmem + (uint32_t)(s * 128 + half * 64) + ((uint32_t)((warp & 3) * 32) << 16);
     const float c2 = sl2 > 0.f ? sl2 : 1.f;
-    const uint32_t done = (half == 0 ? ready : ready2) + 8 * s;  // this half of P is written
+    const uint32_t written = (half == 0 ? ready : ready2) + 8 * s;  // this half of P is
     const int pair = 1 + s * 4 + (warp & 3);  // barrier of the two warps of these rows
     uint32_t sph = 0, fph = 0, oph = 0;
     bool ended = false;  // slot 1's part of a one-tile item, which slot 0 has to read first
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         } else if (any && half == 0 && lane == 0) {  // no rows here: P may hold anything
           mbar_arrive(corr + 8 * s);
         }
-        if (lane == 0) mbar_arrive(done);
+        if (lane == 0) mbar_arrive(written);
         any = true;
       }
       if (!ok) break;

@@ -10,6 +10,7 @@
 namespace qsa {
 
 constexpr int PT_ROWS = 128;                   // tokens (MMA rows) of a tile
+constexpr int PT_MAX_LEN = 1 << 30;            // tokens of a sequence (token arithmetic is 32-bit)
 constexpr uint32_t PT_HALF = PT_ROWS * 128;    // bytes of its 64-value half (128-byte swizzle)
 constexpr uint32_t PT_TILE = 2 * PT_HALF;      // a tile: 128 rows of 128 bf16 values
 

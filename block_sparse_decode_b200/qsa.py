@@ -531,6 +531,8 @@ def qsa_qk_norm_rope(pos, q, k, q_weight, k_weight, eps: float, rope, q_out, k_o
         _shape(k_out, (N, Hk, D), "k_out")
     _shape(q_out, (N, Hq, D), "q_out")
     _shape(pos, (N,), "pos")
+    if rope is not None and rope.dim() != 2:
+        raise ValueError("rope must be [max_pos, rot_dim]")
     for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None:
             _shape(t, (D,), name)

@@ -428,7 +428,7 @@ size_t qsa_chunk_attention_workspace_size(const qsa_dims *dims, int32_t S, int32
  *            calls that may run at the same time need two).
  * Rows outside every chunk stay as they were. So do the rows of a chunk that
  * overruns Nq, is longer than its sequence, or whose sequence is longer than
- * max_pages_per_seq * P tokens; it raises device error flag 16. A page id out
+ * max_pages_per_seq * P (or 2^30) tokens; it raises device error flag 16. A page id out
  * of range raises flag 2 and leaves the values of its sequence's rows
  * undefined. The cache slots past L_s may hold anything; the K and V of
  * tokens below L_s must be finite. 0 <= S, Nq <= 65535. */
@@ -450,7 +450,9 @@ size_t qsa_attention_mass_workspace_size(const qsa_dims *dims, int32_t S, int32_
  *   mass_in  fp32 [S, ld_mass] or NULL (zeros);  mass  fp32 [S, ld_mass], may
  *            be mass_in itself. All ld_mass entries of the S rows are written
  *            (mass_in's value where no row sees a token of the block).
- * The sums are fp32 in a fixed order: the same call gives the same bits. A
+ * The sums are fp32 in a fixed order: the same call gives the same bits. q
+ * and the K of tokens below L_s must be finite. A page id out of range raises
+ * flag 2 and leaves the entries of its tokens undefined. A
  * chunk that qsa_chunk_attention would skip, or whose ceil(L_s / 4) blocks
  * exceed ld_mass, adds nothing and raises device error flag 16. */
 qsa_status qsa_attention_mass(const qsa_dims *dims, const qsa_cache *cache, int32_t S,

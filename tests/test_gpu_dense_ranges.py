@@ -1,0 +1,225 @@
+"""The dense-path calls at the ends of their ranges: many sequences, long
+contexts, unusual scales, queries whose weights do not belong to the LSEs given,
+weights that do not fit the eviction's shared memory, workspaces that two
+captured calls share in order. Tolerances as in test_gpu_dense.py."""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from block_sparse_decode_b200 import qsa
+from tests.test_gpu_dense import DEV, HALF, Paged, attention_ref, evict_ref, randn
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(pc, start, q, out_dtype=torch.float32):
+    b = qsa.alloc_chunk_attention(pc.dims, len(pc.lens), q.shape[0], out_dtype=out_dtype)
+    b.ws.random_(0, 255)
+    qsa.qsa_chunk_attention(pc.dims, pc.cache, pc.seq_lens, start, q, b.out, b.lse, b.ws)
+    assert qsa.qsa_check_device_errors() == 0
+    return b
+
+
+def weigh(pc, start, q, lse, ld=None):
+    m = qsa.alloc_attention_mass(pc.dims, len(pc.lens), q.shape[0], ld or qsa.ld_for(pc.lens))
+    m.ws.random_(0, 255)
+    qsa.qsa_attention_mass(pc.dims, pc.cache, pc.seq_lens, start, q, lse, None, m.mass, m.ws)
+    assert qsa.qsa_check_device_errors() == 0
+    return m.mass
+
+
+def check(pc, chunks, q, b, mass=None):
+    ref, lse, size, w = attention_ref(pc, chunks, q)
+    assert bool(((b.out.double() - ref).abs() <= (HALF + 2.0 ** -12) * size + 1e-6).all())
+    assert float((b.lse.double() - lse).abs().max()) <= 1e-3
+    if mass is not None:
+        for s, want in enumerate(w):
+            got = mass[s, :want.numel()].double()
+            assert bool(((got - want).abs() <= 1e-3 * want + 1e-6).all())
+            assert bool((mass[s, want.numel():] == 0).all())
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-3, 0.5])
+def test_scales(scale):
+    pc = Paged([400, 131], 8, 2, 32, seed=5)
+    pc.dims = qsa.QsaDims(8, 2, 128, 4, 64, 32, scale)
+    start, q = pc.rows([37, 131], 6)
+    b = attend(pc, start, q)
+    check(pc, [37, 131], q, b, weigh(pc, start, q, b.lse))
+
+
+@pytest.mark.parametrize("S,longest,T,Hq,Hkv", [(1300, 90, 1, 8, 2), (1200, 40, 3, 4, 4)])
+def test_many_sequences(S, longest, T, Hq, Hkv):
+    """More sequences (and groups) than the plan has threads; some have no rows."""
+    g = torch.Generator().manual_seed(S)
+    lens = torch.randint(T, longest, (S,), generator=g).tolist()
+    chunks = torch.randint(0, T + 1, (S,), generator=g).tolist()
+    pc = Paged(lens, Hq, Hkv, 16, seed=S)
+    start, q = pc.rows(chunks, 7)
+    b = attend(pc, start, q)
+    check(pc, chunks, q, b, weigh(pc, start, q, b.lse))
+
+
+@pytest.mark.parametrize("lens,chunks,P", [([70001], [1], 64), ([33000, 5], [9, 5], 1024),
+                                           ([8200, 130], [700, 130], 12)])
+def test_long_contexts(lens, chunks, P):
+    pc = Paged(lens, 8, 1, P, seed=11, scale=2.0)
+    start, q = pc.rows(chunks, 8)
+    b = attend(pc, start, q)
+    check(pc, chunks, q, b, weigh(pc, start, q, b.lse))
+
+
+def test_rows_of_chunks_add_up():
+    """The rows of one call, and the same rows in calls of one token each, give
+    the same results (each row of its own causal prefix)."""
+    L, T = 300, 40
+    pc = Paged([L], 16, 2, 64, seed=12)
+    start, q = pc.rows([T], 9)
+    whole = attend(pc, start, q)
+    mass = weigh(pc, start, q, whole.lse, 75)
+    total = torch.zeros_like(mass)
+    for i in range(T):
+        pc.lens = [L - T + i + 1]
+        pc.seq_lens = torch.tensor(pc.lens, dtype=torch.int32, device=DEV)
+        one = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+        b = attend(pc, one, q[i:i + 1].contiguous())
+        # both are within the rounding of the weights of the exact result
+        assert float((b.out[0] - whole.out[i]).abs().max()) <= 2 * HALF * 4
+        assert float((b.lse[0] - whole.lse[i]).abs().max()) <= 1e-4
+        total += weigh(pc, one, q[i:i + 1].contiguous(), b.lse, 75)
+    assert bool(((total - mass).abs() <= 1e-4 * mass + 1e-6).all())
+
+
+def test_weights_of_other_lse():
+    """An LSE that is -inf gives no weight, +inf gives none either, and one below
+    the row's own (as over a selection of blocks) weights above 1, which the sum
+    holds up to 2^127."""
+    pc = Paged([200], 8, 2, 64, seed=13)
+    start, q = pc.rows([4], 10)
+    b = attend(pc, start, q)
+    _, lse, _, _ = attention_ref(pc, [4], q)
+    mine = lse.float().clone()
+    mine[0] = -math.inf
+    mine[1] = math.inf
+    mine[2] -= 20.0
+    mine[3] = -1000.0
+    mine[3, 1:] = -math.inf
+    got = weigh(pc, start, q, mine)
+    assert not bool(got.isnan().any())
+    # row 3, head 0 alone: every weight is past 2^127 and counts as large
+    mine[:3] = -math.inf
+    assert bool((weigh(pc, start, q, mine) >= 2.0 ** 127).all())
+    mine[3] = -math.inf
+    assert bool((weigh(pc, start, q, mine) == 0).all())
+    mine[2] = lse[2].float() - 20.0
+    want = torch.zeros(200, dtype=torch.float64, device=DEV)
+    for h in range(8):
+        z = q[2, h].double() @ pc.k[0][:199, h // 4].double().T * pc.dims.scale
+        want[:199] += torch.exp(z - mine[2, h].double())
+    want = want.view(50, 4).sum(1)
+    assert bool(((weigh(pc, start, q, mine)[0].double() - want).abs() <= 1e-3 * want).all())
+
+
+def test_queries_of_others_do_not_matter():
+    """NaN and infinity in the rows of other chunks and behind the last one reach
+    neither a row's result nor its sequence's weights."""
+    pc = Paged([150, 90, 61], 32, 4, 64, seed=14)
+    start, q = pc.rows([5, 3, 2], 11, extra=3)
+    clean = attend(pc, start, q.clone())
+    want = weigh(pc, start, q, clean.lse)
+    q[5:8] = math.nan
+    q[10:] = math.inf
+    lse = clean.lse.clone()
+    lse[5:8] = math.nan
+    got = attend(pc, start, q)
+    rows = [0, 1, 2, 3, 4, 8, 9]
+    assert torch.equal(got.out[rows], clean.out[rows])
+    assert torch.equal(got.lse[rows], clean.lse[rows])
+    mass = weigh(pc, start, q, lse)
+    assert torch.equal(mass[0], want[0]) and torch.equal(mass[2], want[2])
+
+
+@pytest.mark.parametrize("keep", [3, 40000])
+def test_evict_long_sequences(keep):
+    """More blocks than the selection keeps in shared memory, next to short ones."""
+    lens = [4 * 60001 + 2, 17]
+    P, Hkv = 256, 1
+    per = -(-4 * keep // P)
+    pc = Paged(lens, 4, Hkv, P, 64, seed=keep, spare=2 * per)
+    ld = qsa.ld_for(lens)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    mass = torch.randint(0, 5000, (2, ld), generator=g, device=DEV).float()
+    width = pc.cache.block_table.shape[1]
+    dst = torch.full((2, width), -1, dtype=torch.int32, device=DEV)
+    dst[:, :per] = torch.arange(2 * per, dtype=torch.int32, device=DEV).view(2, per) + pc.first_spare
+    b = qsa.alloc_evict(2, ld, keep)
+    qsa.qsa_evict(pc.dims, pc.cache, pc.seq_lens, mass, keep, 1, 1, dst, b.kept, b.new_lens, b.mass)
+    assert qsa.qsa_check_device_errors() == 0
+    for s, want in enumerate(evict_ref(lens, mass, keep, 1, 1)):
+        assert b.kept[s, :len(want)].tolist() == want
+        w = torch.tensor(want, device=DEV)
+        nl = int(b.new_lens[s])
+        assert nl == 4 * len(want) - (-lens[s]) % 4
+        t = torch.arange(nl, device=DEV)
+        page, slot = pc.places(dst, s, nl, P)
+        assert torch.equal(pc.cache.k_pool[page, slot], pc.k[s][4 * w[t // 4] + t % 4])
+
+
+def test_one_workspace_in_turn():
+    """Two captured calls that share a workspace and run one after the other,
+    replayed in either order, and an eager call between them."""
+    pc = Paged([900, 40], 32, 4, 64, seed=15)
+    a_start, a_q = pc.rows([33, 40], 1)
+    b_start, b_q = pc.rows([1, 1], 2)
+    a = qsa.alloc_chunk_attention(pc.dims, 2, 73)
+    b = qsa.alloc_chunk_attention(pc.dims, 2, 2)
+    ws = a.ws if a.ws.numel() >= b.ws.numel() else b.ws
+
+    def call(start, q, buf):
+        qsa.qsa_chunk_attention(pc.dims, pc.cache, pc.seq_lens, start, q, buf.out, buf.lse, ws)
+
+    call(a_start, a_q, a)
+    call(b_start, b_q, b)
+    torch.cuda.synchronize()
+    want = a.out.clone(), b.out.clone()
+    graphs = []
+    for args in ((a_start, a_q, a), (b_start, b_q, b)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(*args)
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (1, 1, 0)):
+        a.out.zero_(), b.out.zero_()
+        for i in order:
+            graphs[i].replay()
+            call(b_start, b_q, b)
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+
+
+def test_norm_rope_zero_rows_and_repeats():
+    """Rows of zeros stay zero (eps > 0); the same position twice, and position 0."""
+    q = torch.zeros((5, 4, 128), dtype=torch.bfloat16, device=DEV)
+    q[1:] = randn((4, 4, 128), 3)
+    q[2] = q[1]
+    pos = torch.tensor([9, 5, 5, 0, 5], dtype=torch.int32, device=DEV)
+    w = torch.rand(128, device=DEV)
+    out = torch.empty_like(q)
+    qsa.qsa_qk_norm_rope(pos, q, None, w, None, 1e-6, qsa.rope_table(10, 64), out)
+    assert bool((out[0] == 0).all()) and torch.equal(out[1], out[2])
+    y = q[3].float() * torch.rsqrt(q[3].float().square().mean(-1, keepdim=True) + 1e-6) * w
+    assert bool(((out[3].float() - y).abs() <= HALF * y.abs() + 1e-6).all())
+
+
+def test_other_devices_are_refused(monkeypatch):
+    """Tensors of a device that is not the current one: refused, not launched."""
+    q = randn((1, 2, 64), 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: q.device.index + 1)
+    with pytest.raises(ValueError, match="current device"):
+        qsa.qsa_qk_norm_rope(torch.zeros(1, dtype=torch.int32, device=DEV), q, None, None, None,
+                             0.0, None, torch.empty_like(q))
