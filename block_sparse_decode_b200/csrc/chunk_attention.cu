@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         for (int at = 0;; ++at) {
           const int i = at % CA_ITEMS;
           if (!wait_bar(smem_u32(&ctl.iempty[i]), (uint32_t)((at / CA_ITEMS) & 1) ^ 1u, abort_flag,
-                         p.err))
+                        p.err, PT_LONG_ROUNDS))
             break;
           CaItem &it = ctl.item[i];
           it.a = it.b = 0;
@@ -948,7 +948,9 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           if (!more) break;
           // the item's query tiles, once the one before it has used its own
           // (its K and V tiles are on their way already)
-          if (at > 0 && !wait_bar(qempty, (uint32_t)(at - 1) & 1u, abort_flag, p.err)) break;
+          if (at > 0 &&
+              !wait_bar(qempty, (uint32_t)(at - 1) & 1u, abort_flag, p.err, PT_LONG_ROUNDS))
+            break;
           const int tiles = w.w == 2 ? 2 : 1;
           if (w.gi.z <= CA_FEW) {  // one by one: the tile's other rows stay zero
             mbar_arrive_expect(qfull, (uint32_t)(w.gi.z * p.G * 256));

@@ -57,10 +57,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // Bounded wait, as mbar_wait, but a round may sleep up to PT_WAIT_NS until the
 // phase completes: the other warps' polling would take issue slots and
 // instruction fetches from the softmax.
-constexpr uint32_t PT_WAIT_NS = 20000, PT_WAIT_ROUNDS = 1u << 16;
+// A round that nothing ends takes 4 us: PT_WAIT_ROUNDS are 0.27 s. A wait for a
+// whole item of up to 2^30 tokens (2^23 steps, 18 s) takes PT_LONG_ROUNDS, 34 s;
+// when another role gives up, it ends within a round.
+constexpr uint32_t PT_WAIT_NS = 20000, PT_WAIT_ROUNDS = 1u << 16, PT_LONG_ROUNDS = 1u << 23;
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                        unsigned *err) {
-  for (uint32_t i = 0; i < PT_WAIT_ROUNDS; ++i) {
+                                         unsigned *err, uint32_t rounds = PT_WAIT_ROUNDS) {
+  for (uint32_t i = 0; i < rounds; ++i) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"

@@ -5,6 +5,7 @@ captured calls share in order. Tolerances as in test_gpu_dense.py."""
 
 from __future__ import annotations
 
+import dataclasses
 import math
 
 import pytest
@@ -71,6 +72,28 @@ def test_long_contexts(lens, chunks, P):
     start, q = pc.rows(chunks, 8)
     b = attend(pc, start, q)
     check(pc, chunks, q, b, weigh(pc, start, q, b.lse))
+
+
+def test_long_items():
+    """Items of 2^19 key tiles, longer than any wait for one tile may last. Every
+    page of a sequence is the same one, so its LSE is that page's, plus ln(pages).
+    A row's sum adds 2^19 partial sums in fp32, split over two halves of the tile
+    and over blocks: each addition is off by 2^-24 of the sum, 2^-5 in all."""
+    P, L, S = 1024, 2 ** 26, 160
+    pc = Paged([P], 8, 1, P, seed=21)
+    start, q = pc.rows([1], 9)
+    near = attend(pc, start, q)
+    table = torch.full((S, L // P), int(pc.cache.block_table[0, 0]), dtype=torch.int32, device=DEV)
+    cache = dataclasses.replace(pc.cache, block_table=table)
+    lens = torch.full((S,), L, dtype=torch.int32, device=DEV)
+    row_start = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+    b = qsa.alloc_chunk_attention(pc.dims, S, S, out_dtype=torch.float32)
+    qsa.qsa_chunk_attention(pc.dims, cache, lens, row_start, q.expand(S, -1, -1).contiguous(),
+                            b.out, b.lse, b.ws)
+    assert qsa.qsa_check_device_errors() == 0
+    want = near.lse.double() + math.log(L // P)
+    assert float((b.lse.double() - want).abs().max()) <= 2.0 ** -5 + 1e-3
+    assert bool(torch.isfinite(b.out).all())
 
 
 def test_rows_of_chunks_add_up():
