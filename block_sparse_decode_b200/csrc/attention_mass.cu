@@ -23,8 +23,10 @@
 // weigh: two K tiles of 128 tokens stay in shared memory for a head while the
 // query blocks stream past them (each query block from L2 serves 256 tokens,
 // 16 bytes a clock per SM), so prompts are bound by the exponentials: 16 a
-// clock per SM, 2,048 clocks a step of 256 x 128. One decode token per
-// sequence is bound by reading K once.
+// clock per SM, 2,048 clocks a step of 256 x 128. A quarter of them goes to the
+// fp32 units instead: 8,192 rows of a prompt (32 query heads) 375 us without,
+// 363 with an eighth, 354 with a quarter. One decode token per sequence is
+// bound by reading K once: 180 us for 32 x 32,768 tokens, 6.0 TB/s.
 //   warps 0-7, 8-15 the weights of the even and the odd steps (S^T is double
 //                   buffered), 4 warps for each of the two K tiles
 //   warp 16         issues the MMAs
@@ -51,7 +53,7 @@ constexpr int AM_QST = 3;      // query blocks
 constexpr int AM_ITEMS = 3;    // items announced ahead
 constexpr int AM_READERS = 19;
 constexpr int AM_TOK = 2 * PT_ROWS;  // tokens of an item
-constexpr uint32_t AM_CTL = 3072;
+constexpr uint32_t AM_CTL = 3 * 1024;
 constexpr size_t AM_SMEM = AM_CTL + (size_t)(2 * AM_KBUF + AM_QST) * PT_TILE;
 constexpr int AM_PLAN_THREADS = 1024;
 constexpr int AM_POLY = 2;  // of 8 pairs of exponentials, those on the fp32 units

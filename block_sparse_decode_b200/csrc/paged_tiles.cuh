@@ -55,8 +55,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 }
 
 // Bounded wait, as mbar_wait, but a round may sleep up to PT_WAIT_NS until the
-// phase completes: the other warps' polling would take issue slots and
-// instruction fetches from the softmax.
+// phase completes, and rounds are 20 ns apart: the other warps' polling takes
+// issue slots from the softmax (ragged chunks 248 us without the pause, 228 with
+// it and no less with a longer one).
 // A round that nothing ends takes 4 us: PT_WAIT_ROUNDS are 0.27 s. A wait for a
 // whole item of up to 2^30 tokens (2^23 steps, 18 s) takes PT_LONG_ROUNDS, 34 s;
 // when another role gives up, it ends within a round.
@@ -72,7 +73,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         : "r"(bar), "r"(parity), "r"(PT_WAIT_NS)
         : "memory");
     if (done) return true;
-    __nanosleep(20);  // (polling slows the warps that compute: ragged chunks 237 us without)
+    __nanosleep(20);
     if (*abort_flag) return false;
   }
   *abort_flag = 1;
