@@ -109,6 +109,15 @@ def test_evict_refusals(L, change, status):
     assert L.qsa_last_error().decode()
 
 
+@pytest.mark.parametrize("change", [dict(ld=2 ** 28 + 1), dict(keep=2 ** 28 + 1),
+                                    dict(ld=2 ** 31 - 1), dict(keep=2 ** 31 - 1)])
+def test_evict_sizes_past_the_indexes(L, change):
+    a = dict(dims=dims(), cache=cache(), B=2, lens=16, mass=32, ld=64, keep=8, sink=4, recent=4,
+             dst=48, kept=64, new=80, mass_out=96, ws=None, ws_bytes=0, stream=None)
+    assert call(L.qsa_evict, {**a, **change}) == qsa.QSA_ERR_UNSUPPORTED
+    assert L.qsa_last_error().decode()
+
+
 def test_calls_on_nothing(L):
     a = dict(CHUNK, out=None, bf16=1, lse=None, ws=None, ws_bytes=0, stream=None)
     assert call(L.qsa_chunk_attention, {**a, "S": 0}) == qsa.QSA_OK
