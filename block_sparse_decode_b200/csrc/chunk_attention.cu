@@ -623,7 +623,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         continue;
       }
       // the item's end: the row's sum over both halves, then this half of the
-      // result's columns, once the slot's last product is in
+      // result's columns, once the slot's last product is in. (First both warps
+      // have to have read the last step's maxima, which the sums overwrite: no
+      // further scores follow that would have waited for it.)
+      both(true);
       ctl.pm[s][half][r] = l;
       both(true);
       l += ctl.pm[s][half ^ 1][r];

@@ -96,6 +96,29 @@ def test_long_items():
     assert bool(torch.isfinite(b.out).all())
 
 
+@pytest.mark.parametrize("longest,T", [(128, 1), (256, 1), (128, 40)])
+def test_short_items_repeat(longest, T):
+    """Items of one or two steps, one behind the other in every CTA: an item's
+    sums take the place of its last maxima, and the next item's maxima theirs.
+    The results are right, and the same bits call after call."""
+    g = torch.Generator().manual_seed(longest + T)
+    S = 600
+    lens = torch.randint(T, longest + 1, (S,), generator=g).tolist()
+    pc = Paged(lens, 32, 4, 64, seed=40, scale=2.0)
+    start, q = pc.rows([T] * S, 12, 1.5)
+    b = attend(pc, start, q)
+    few = 24  # (the sequences with a reference)
+    part = Paged(lens[:few], 32, 4, 64, seed=40, scale=2.0)
+    check(part, [T] * few, q[:few * T],
+          qsa.ChunkBuffers(b.out[:few * T], b.lse[:few * T], b.ws))
+    out, lse = b.out.clone(), b.lse.clone()
+    for _ in range(20):
+        b.out.fill_(math.nan)
+        qsa.qsa_chunk_attention(pc.dims, pc.cache, pc.seq_lens, start, q, b.out, b.lse, b.ws)
+        assert torch.equal(b.out, out) and torch.equal(b.lse, lse)
+    assert qsa.qsa_check_device_errors() == 0
+
+
 def test_rows_of_chunks_add_up():
     """The rows of one call, and the same rows in calls of one token each, give
     the same results (each row of its own causal prefix)."""
