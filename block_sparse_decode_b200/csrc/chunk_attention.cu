@@ -917,6 +917,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
             bool in = true;
             if (lane == 0) in = mbar_wait(vraw, vph, abort_flag, p.err, TC_SPIN_LIMIT, false);
             ok = __shfl_sync(0xffffffffu, in, 0);
+            __syncwarp();  // (the copies are in for every lane)
             vph ^= 1u;
             if (!ok) break;
             for (int i = nrow * 8 + lane; i < CA_KT * 8; i += 32)

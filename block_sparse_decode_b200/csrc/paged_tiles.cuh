@@ -109,12 +109,14 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Whole-warp bounded wait: lane 0 polls.
+// Whole-warp bounded wait: lane 0 polls. What it has seen complete is ordered
+// before the other lanes' accesses by __syncwarp; a shuffle alone orders none.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                              unsigned *err) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, abort_flag, err);
   ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
   return ok;
 }
 
