@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           sph ^= 1u;
           tc_fence_after();
           // the first column that sees the token: row i sees its first before + i + 1
-          const int c0 = (t - before - qb * p.TT) * p.G;
+          // (a token can lie 2^30 before the rows, which times G passes 32 bits;
+          // from 32 before them on, every lane's first column is below 0 either way)
+          const int c0 = max(t - before - qb * p.TT, -32) * p.G;
           // (lanes are consecutive tokens: the warp's least and largest)
           const int cmin = __shfl_sync(0xffffffffu, c0, 0), cmax = cmin + 31 * p.G;
           unsigned long long la = f2_pack(0.f, 0.f), lb = la;

@@ -119,6 +119,35 @@ def test_short_items_repeat(longest, T):
     assert qsa.qsa_check_device_errors() == 0
 
 
+@pytest.mark.parametrize("L,Hq", [(2 ** 28 + 2 ** 17 + 5, 8), (2 ** 30, 8), (2 ** 30, 5)])
+def test_mass_far_before_the_chunk(L, Hq):
+    """Tokens more than 2^28 before the rows, up to the longest sequence there may
+    be. The queries are zero, so every weight of row i is 1 / (the tokens it sees).
+    Every page of the sequence is the same one. The LSE is rounded to 24 bits, off
+    by at most 2^-20 (it is below 32: half a step of 2^-19), and scaled by log2(e):
+    as much again. With the exponential's and the sums' roundings 2^-17 holds all."""
+    P, T = 1024, 3
+    pc = Paged([P], Hq, 1, P, seed=22)
+    pages = -(-L // P)
+    table = pc.cache.block_table[:1, :1].expand(1, pages).contiguous()
+    cache = dataclasses.replace(pc.cache, block_table=table)
+    q = torch.zeros((T, Hq, 128), dtype=torch.bfloat16, device=DEV)
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    start = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    sees = [L - T + i + 1 for i in range(T)]
+    lse = torch.tensor(sees, dtype=torch.float64, device=DEV).log().float()[:, None]
+    lse = lse.expand(T, Hq).contiguous()
+    m = qsa.alloc_attention_mass(pc.dims, 1, T, -(-L // 4))
+    qsa.qsa_attention_mass(pc.dims, cache, lens, start, q, lse, None, m.mass, m.ws)
+    assert qsa.qsa_check_device_errors() == 0
+    whole = (L - T) // 4  # blocks that every row sees
+    want = 4 * Hq * sum(1 / n for n in sees)
+    assert float((m.mass[0, :whole] - want).abs().max()) <= 2.0 ** -17 * want
+    for j in range(whole, -(-L // 4)):
+        want = Hq * sum(max(0, min(4, n - 4 * j)) / n for n in sees)
+        assert abs(float(m.mass[0, j]) - want) <= 2.0 ** -17 * want
+
+
 def test_rows_of_chunks_add_up():
     """The rows of one call, and the same rows in calls of one token each, give
     the same results (each row of its own causal prefix)."""
