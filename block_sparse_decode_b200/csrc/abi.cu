@@ -599,21 +599,26 @@ qsa_status qsa_qk_norm_rope(int32_t N, int32_t Hq, int32_t Hk, int32_t D, const 
 
 namespace {
 
-// Checks shared by the calls over the rows of appended chunks.
-qsa_status check_chunks(const qsa_dims *dims, const qsa_cache *cache, int32_t S, int32_t Nq) {
+// Checks shared by the calls over the rows of appended chunks and by the
+// queries of their workspaces (no scratch where the call refuses the sizes).
+qsa_status check_chunk_sizes(const qsa_dims *dims, int32_t S, int32_t Nq) {
   QSA_TRY(check_dims(dims));
-  QSA_TRY(check_cache(cache, true, false));
-  if (S < 0 || S > 65535 || S > cache->num_seqs)
-    return fail(QSA_ERR_INVALID_ARG, "S=%d outside [0, 65535] or over the block_table rows %d", S,
-                cache->num_seqs);
+  if (S < 0 || S > 65535) return fail(QSA_ERR_INVALID_ARG, "S=%d outside [0, 65535]", S);
   if (Nq < 0 || Nq > 65535) return fail(QSA_ERR_INVALID_ARG, "Nq=%d outside [0, 65535]", Nq);
+  return QSA_OK;
+}
+qsa_status check_chunks(const qsa_dims *dims, const qsa_cache *cache, int32_t S, int32_t Nq) {
+  QSA_TRY(check_chunk_sizes(dims, S, Nq));
+  QSA_TRY(check_cache(cache, true, false));
+  if (S > cache->num_seqs)
+    return fail(QSA_ERR_INVALID_ARG, "S=%d over the block_table rows %d", S, cache->num_seqs);
   return QSA_OK;
 }
 
 }  // namespace
 
 size_t qsa_chunk_attention_workspace_size(const qsa_dims *dims, int32_t S, int32_t Nq) {
-  if (dims == nullptr || S <= 0 || Nq <= 0 || dims->Hkv <= 0 || dims->Hq <= 0) return 0;
+  if (check_chunk_sizes(dims, S, Nq) != QSA_OK || S == 0 || Nq == 0) return 0;
   return chunk_attention_ws_bytes(*dims, S, Nq);
 }
 
@@ -643,7 +648,7 @@ qsa_status qsa_chunk_attention(const qsa_dims *dims, const qsa_cache *cache, int
 }
 
 size_t qsa_attention_mass_workspace_size(const qsa_dims *dims, int32_t S, int32_t Nq) {
-  if (dims == nullptr || S <= 0 || Nq <= 0 || dims->Hkv <= 0 || dims->Hq <= 0) return 0;
+  if (check_chunk_sizes(dims, S, Nq) != QSA_OK || S == 0 || Nq == 0) return 0;
   return attention_mass_ws_bytes(*dims, S, Nq);
 }
 

@@ -95,6 +95,19 @@ def test_workspaces_are_asked_for(L):
         assert f(None, 2, 5) == 0 and f(ctypes.byref(dims()), 0, 5) == 0
 
 
+@pytest.mark.parametrize("change", [
+    dict(Hq=2, Hkv=4), dict(Hq=1, Hkv=3), dict(Hq=256, Hkv=1), dict(Hq=6, Hkv=4), dict(Hq=0),
+    dict(Hkv=0), dict(Hkv=-1), dict(D=64), dict(P=6), dict(S=65536), dict(S=2 ** 31 - 1), dict(S=-1),
+    dict(Nq=65536), dict(Nq=2 ** 31 - 1), dict(Nq=-1)])
+def test_workspaces_of_refused_calls_are_empty(L, change):
+    """Sizes and dims that the calls refuse need no scratch (and end no process)."""
+    sizes = dict(S=2, Nq=5)
+    sizes.update({k: v for k, v in change.items() if k in sizes})
+    d = qsa._Dims(*{**DIMS, **{k: v for k, v in change.items() if k in DIMS}}.values())
+    for f in (L.qsa_chunk_attention_workspace_size, L.qsa_attention_mass_workspace_size):
+        assert f(ctypes.byref(d), sizes["S"], sizes["Nq"]) == 0
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(dims=dims(di=96)), UNS), (dict(cache=cache(k=None)), BAD), (dict(B=5), BAD),
     (dict(B=-1), BAD), (dict(ld=0), UNS), (dict(keep=0), UNS), (dict(sink=-1), BAD),
