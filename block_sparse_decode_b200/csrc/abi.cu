@@ -648,7 +648,8 @@ qsa_status qsa_chunk_attention(const qsa_dims *dims, const qsa_cache *cache, int
 }
 
 size_t qsa_attention_mass_workspace_size(const qsa_dims *dims, int32_t S, int32_t Nq) {
-  if (check_chunk_sizes(dims, S, Nq) != QSA_OK || S == 0 || Nq == 0) return 0;
+  // (without rows the call still plans, for its flags, and copies mass_in)
+  if (check_chunk_sizes(dims, S, Nq) != QSA_OK || S == 0) return 0;
   return attention_mass_ws_bytes(*dims, S, Nq);
 }
 

@@ -95,6 +95,16 @@ def test_workspaces_are_asked_for(L):
         assert f(None, 2, 5) == 0 and f(ctypes.byref(dims()), 0, 5) == 0
 
 
+def test_workspace_without_rows(L):
+    """The mass copies mass_in where there are no rows; the scratch it then asks
+    for is what its query says."""
+    need = L.qsa_attention_mass_workspace_size(ctypes.byref(dims()), 2, 0)
+    a = dict(CHUNK, lse=None, mass_in=None, mass=16, ld=64, ws=16, ws_bytes=0, stream=None)
+    a.update(Nq=0, q=None)
+    assert call(L.qsa_attention_mass, a) == BAD
+    assert f"workspace 0 bytes < {need} needed" in L.qsa_last_error().decode()
+
+
 @pytest.mark.parametrize("change", [
     dict(Hq=2, Hkv=4), dict(Hq=1, Hkv=3), dict(Hq=256, Hkv=1), dict(Hq=6, Hkv=4), dict(Hq=0),
     dict(Hkv=0), dict(Hkv=-1), dict(D=64), dict(P=6), dict(S=65536), dict(S=2 ** 31 - 1), dict(S=-1),

@@ -148,6 +148,29 @@ def test_mass_far_before_the_chunk(L, Hq):
         assert abs(float(m.mass[0, j]) - want) <= 2.0 ** -17 * want
 
 
+def test_mass_without_rows():
+    """No rows at all: mass is mass_in (or zeros, or itself), and a chunk that
+    reaches past the rows is still flagged."""
+    pc = Paged([100, 40], 8, 2, 64, seed=23)
+    start, q = pc.rows([0, 0], 1)
+    assert q.shape[0] == 0
+    m = qsa.alloc_attention_mass(pc.dims, 2, 0, 25)
+    lse = torch.empty((0, 8), device=DEV)
+    base = torch.rand((2, 25), device=DEV)
+    for given, want in ((base, base), (None, torch.zeros_like(base))):
+        m.mass.fill_(math.nan)
+        qsa.qsa_attention_mass(pc.dims, pc.cache, pc.seq_lens, start, q, lse, given, m.mass, m.ws)
+        assert torch.equal(m.mass, want)
+    again = base.clone()
+    qsa.qsa_attention_mass(pc.dims, pc.cache, pc.seq_lens, start, q, lse, again, again, m.ws)
+    assert torch.equal(again, base) and qsa.qsa_check_device_errors() == 0
+    start[2] = 1
+    qsa.qsa_attention_mass(pc.dims, pc.cache, pc.seq_lens, start, q, lse, base, m.mass, m.ws)
+    with pytest.raises(qsa.QsaError, match="flags=16"):
+        qsa.qsa_check_device_errors()
+    assert torch.equal(m.mass, base)
+
+
 def test_rows_of_chunks_add_up():
     """The rows of one call, and the same rows in calls of one token each, give
     the same results (each row of its own causal prefix)."""
