@@ -655,15 +655,17 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         m1 = ctl.pm[1][1][r];
       }
       if (ok && live) {
-        const float M = fmaxf(l > 0.f ? m : -INFINITY, l1 > 0.f ? m1 : -INFINITY);
-        const float e0 = l > 0.f ? ex2_approx(m - M) : 0.f;
-        const float e1 = l1 > 0.f ? ex2_approx(m1 - M) : 0.f;
+        // (a sum of 0: nothing seen, or no weight above 0 here. One that is NaN,
+        // from a score that is NaN or +inf, goes on to the result and its LSE)
+        const float M = fmaxf(l != 0.f ? m : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
+        const float e0 = l != 0.f ? ex2_approx(m - M) : 0.f;
+        const float e1 = l1 != 0.f ? ex2_approx(m1 - M) : 0.f;
         const float sum = e0 * l + e1 * l1;
-        const float f0 = sum > 0.f ? e0 / sum : 0.f, f1 = sum > 0.f ? e1 / sum : 0.f;
+        const float f0 = sum != 0.f ? e0 / sum : 0.f, f1 = sum != 0.f ? e1 / sum : 0.f;
         const bool whole = it.whole != 0;
         const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
         if (valid && half == 0) {
-          const float lse = sum > 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          const float lse = sum != 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           if (!whole) p.rec_lse[rec] = lse;
           else if (p.lse != nullptr) p.lse[row] = lse;
         }
@@ -675,13 +677,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           tc_ld32_nowait(to + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = f0 > 0.f ? o[i] * f0 : 0.f;
+          for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? o[i] * f0 : 0.f;
           if (has1) {
 #pragma unroll
             for (int k = 0; k < 32; k += 16) {
               float o1[16];
               tc_ld16(to + 128 + 32 * c + k, o1);
-              if (f1 > 0.f) {
+              if (f1 != 0.f) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[k + i] = fmaf(o1[i], f1, o[k + i]);
               }
@@ -1029,28 +1031,28 @@ __global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M > -INFINITY) {
-      for (int c = c0; c <= c1; c += 4) {
-        float f[4];
-        float4 v[4];
+    // (fmaxf passes over a part whose LSE is NaN; its factor is NaN)
+    for (int c = c0; c <= c1; c += 4) {
+      float f[4];
+      float4 v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          f[u] = c + u <= c1 ? __expf(__ldcg(p.rec_lse + rec(c + u)) - M) : 0.f;
-          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (f[u] > 0.f)
-            v[u] = __ldcg(reinterpret_cast<const float4 *>(p.rec_o + rec(c + u) * CA_D) + lane);
-        }
+      for (int u = 0; u < 4; ++u) {
+        const float e = c + u <= c1 ? __ldcg(p.rec_lse + rec(c + u)) : -INFINITY;
+        f[u] = e == -INFINITY ? 0.f : __expf(e - M);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (f[u] != 0.f)
+          v[u] = __ldcg(reinterpret_cast<const float4 *>(p.rec_o + rec(c + u) * CA_D) + lane);
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          sum += f[u];
-          acc.x = fmaf(f[u], v[u].x, acc.x);
-          acc.y = fmaf(f[u], v[u].y, acc.y);
-          acc.z = fmaf(f[u], v[u].z, acc.z);
-          acc.w = fmaf(f[u], v[u].w, acc.w);
-        }
+      for (int u = 0; u < 4; ++u) {
+        sum += f[u];
+        acc.x = fmaf(f[u], v[u].x, acc.x);
+        acc.y = fmaf(f[u], v[u].y, acc.y);
+        acc.z = fmaf(f[u], v[u].z, acc.z);
+        acc.w = fmaf(f[u], v[u].w, acc.w);
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const size_t row = (size_t)(gi.y + i / p.G) * p.Hq + (size_t)h * p.G + i % p.G;
     acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
     if (p.out_bf16)
@@ -1058,7 +1060,7 @@ __global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
           make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
     else
       reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * CA_D)[lane] = acc;
-    if (lane == 0 && p.lse != nullptr) p.lse[row] = sum > 0.f ? M + logf(sum) : -INFINITY;
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = sum != 0.f ? M + logf(sum) : -INFINITY;
   }
 }
 

@@ -431,7 +431,9 @@ size_t qsa_chunk_attention_workspace_size(const qsa_dims *dims, int32_t S, int32
  * max_pages_per_seq * P (or 2^30) tokens; it raises device error flag 16. A page id out
  * of range raises flag 2 and leaves the values of its sequence's rows
  * undefined. The cache slots past L_s may hold anything; the K and V of
- * tokens below L_s must be finite. 0 <= S, Nq <= 65535. */
+ * tokens below L_s must be finite. A row and head with a score (fp32) that is
+ * NaN or +infinity gets NaN, its LSE too; one whose scores are all -infinity
+ * zeros and LSE -infinity. 0 <= S, Nq <= 65535. */
 qsa_status qsa_chunk_attention(const qsa_dims *dims, const qsa_cache *cache, int32_t S,
                                const int32_t *seq_lens, const int32_t *row_start, int32_t Nq,
                                const void *q, void *out, int32_t out_is_bf16, float *lse_out,

@@ -241,6 +241,57 @@ def test_queries_of_others_do_not_matter():
     assert torch.equal(mass[0], want[0]) and torch.equal(mass[2], want[2])
 
 
+@pytest.mark.parametrize("lens,chunks,Hq,Hkv", [
+    ([70001], [1], 8, 2), ([3000, 200], [1, 1], 32, 4), ([515, 70], [90, 70], 16, 4),
+    ([5000], [40], 32, 4), ([130] * 300, [1] * 300, 8, 2), ([700], [257], 5, 1), ([20000], [33], 8, 1)])
+def test_scores_that_are_not_finite(lens, chunks, Hq, Hkv):
+    """A head of a row whose scores hold NaN or +infinity gets NaN, as its formula
+    does, whoever works on that part of its tokens; a score of -infinity is a
+    weight of 0. The other rows and heads keep their bits."""
+    pc = Paged(lens, Hq, Hkv, 64, seed=41)
+    start, q = pc.rows(chunks, 13)
+    for s, (n, T) in enumerate(zip(lens, chunks)):
+        pc.k[s][:, :, 0] = 0
+        pc.k[s][(n - T) // 2, :, 0] = 2.0  # one token, seen by every row
+        page, slot = pc.places(pc.cache.block_table, s, n, 64)
+        pc.cache.k_pool[page, slot] = pc.k[s]
+    rows = [int(start[s]) + T - 1 - T // 3 for s, T in enumerate(chunks)]
+    q[rows, 3] = 0
+    clean = attend(pc, start, q)
+    q[rows, 0] = math.nan
+    q[rows, 1, 5] = math.inf
+    q[rows, 2] = 0
+    q[rows, 2, 0] = 3e38  # 6e38 for the one token: past the scores' range
+    q[rows, 3, 0] = -3e38
+    got = attend(pc, start, q)
+    bad = torch.zeros((q.shape[0], Hq), dtype=torch.bool, device=DEV)
+    for h in range(3):
+        bad[rows, h] = True
+    assert bool(got.out[bad].isnan().all()) and bool(got.lse[bad].isnan().all())
+    bad[rows, 3] = True
+    assert torch.equal(got.out[~bad], clean.out[~bad])
+    assert torch.equal(got.lse[~bad], clean.lse[~bad])
+    ref, lse, size, _ = attention_ref(pc, chunks, q)  # (in 64 bits the score is finite)
+    err = (got.out[rows, 3].double() - ref[rows, 3]).abs()
+    assert bool((err <= (HALF + 2.0 ** -12) * size[rows, 3] + 1e-6).all())
+    assert float((got.lse[rows, 3].double() - lse[rows, 3]).abs().max()) <= 1e-3
+
+
+def test_rows_without_any_weight():
+    """All scores -infinity: no weight, as where nothing is seen."""
+    pc = Paged([300, 70], 8, 2, 64, seed=42)
+    for s, n in enumerate(pc.lens):
+        pc.k[s][:, :, 0] = 2.0
+        page, slot = pc.places(pc.cache.block_table, s, n, 64)
+        pc.cache.k_pool[page, slot] = pc.k[s]
+    start, q = pc.rows([1, 70], 14)
+    q[:, ::2] = 0
+    q[:, ::2, 0] = -3e38
+    b = attend(pc, start, q)
+    assert bool((b.out[:, ::2] == 0).all()) and bool((b.lse[:, ::2] == -math.inf).all())
+    assert bool(torch.isfinite(b.lse[:, 1::2]).all())
+
+
 @pytest.mark.parametrize("keep", [3, 40000])
 def test_evict_long_sequences(keep):
     """More blocks than the selection keeps in shared memory, next to short ones."""
