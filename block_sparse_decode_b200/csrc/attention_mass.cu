@@ -191,16 +191,19 @@ __device__ long long am_find(const AmArgs &p, long long at, AmItem &it) {
 
 // ------------------------------------------------------------------ weigh
 
-// 2^x of a pair on the fp32 units: x = n + f with n the nearest whole number
-// (left in the low bits of x + 1.5 * 2^23) and |f| <= 1/2, 2^f by the polynomial
-// 1 + f (c1 + ... c5 f^4) of least relative error there (a linear program on a
-// grid; 1.7e-7 with its fp32 roundings), and n added to its exponent. x below
-// -127 counts as -127, whose 2^x is then exactly 0; x above 127 counts as 127.
-__device__ __forceinline__ unsigned long long exp2_poly(unsigned long long x) {
-  float x0, x1;
-  f2_unpack(x, x0, x1);
-  const float m0 = fminf(fmaxf(x0, -127.f), 127.f), m1 = fminf(fmaxf(x1, -127.f), 127.f);
-  const unsigned long long m = f2_pack(m0, m1);
+// sum + 2^x of a pair on the fp32 units: x = n + f with n the nearest whole
+// number (left in the low bits of x + 1.5 * 2^23) and |f| <= 1/2, 2^f by the
+// polynomial 1 + f (c1 + ... c5 f^4) of least relative error there (a linear
+// program on a grid; 1.7e-7 with its fp32 roundings), and 2^n, whose bits are n
+// in the exponent's place, in the multiplication that adds to the sum. x is held
+// in [-127, 128], where 2^n is exactly 0 and infinity; a NaN stays one.
+__device__ __forceinline__ float nan_clamp(float x) {
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;\n min.NaN.f32 %0, %0, 0f43000000;" : "+f"(x));
+  return x;
+}
+__device__ __forceinline__ unsigned long long add_exp2_poly(unsigned long long sum, float x0,
+                                                            float x1) {
+  const unsigned long long m = f2_pack(nan_clamp(x0), nan_clamp(x1));
   const unsigned long long r = f2_add(m, f2_pack(12582912.f, 12582912.f));
   const unsigned long long f =
       f2_fma(f2_add(r, f2_pack(-12582912.f, -12582912.f)), f2_pack(-1.f, -1.f), m);
@@ -210,11 +213,11 @@ __device__ __forceinline__ unsigned long long exp2_poly(unsigned long long x) {
   y = f2_fma(f, y, f2_pack(0x1.ebf9bcp-3f, 0x1.ebf9bcp-3f));
   y = f2_fma(f, y, f2_pack(0x1.62e42ap-1f, 0x1.62e42ap-1f));
   y = f2_fma(f, y, f2_pack(1.f, 1.f));
-  float r0, r1, y0, y1;
+  float r0, r1;
   f2_unpack(r, r0, r1);
-  f2_unpack(y, y0, y1);
-  return f2_pack(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(r0) << 23)),
-                 __uint_as_float(__float_as_uint(y1) + (__float_as_uint(r1) << 23)));
+  return f2_fma(y, f2_pack(__uint_as_float((__float_as_uint(r0) << 23) + 0x3f800000u),
+                           __uint_as_float((__float_as_uint(r1) << 23) + 0x3f800000u)),
+                sum);
 }
 
 struct AmCtrl {
@@ -370,12 +373,12 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              la = f2_add(la, (i / 2) % 8 < AM_POLY
-                                  ? exp2_poly(f2_pack(e[i], e[i + 1]))
-                                  : f2_pack(ex2_approx(e[i]), ex2_approx(e[i + 1])));
-              lb = f2_add(lb, (i / 2 + 1) % 8 < AM_POLY
-                                  ? exp2_poly(f2_pack(e[i + 2], e[i + 3]))
-                                  : f2_pack(ex2_approx(e[i + 2]), ex2_approx(e[i + 3])));
+              la = (i / 2) % 8 < AM_POLY
+                       ? add_exp2_poly(la, e[i], e[i + 1])
+                       : f2_add(la, f2_pack(ex2_approx(e[i]), ex2_approx(e[i + 1])));
+              lb = (i / 2 + 1) % 8 < AM_POLY
+                       ? add_exp2_poly(lb, e[i + 2], e[i + 3])
+                       : f2_add(lb, f2_pack(ex2_approx(e[i + 2]), ex2_approx(e[i + 3])));
             }
           }
           tc_fence_before();
@@ -387,9 +390,9 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           float a0, a1, b0, b1;
           f2_unpack(la, a0, a1);
           f2_unpack(lb, b0, b1);
-          // the sum with what its last rounding lost
+          // the sum with what its last rounding lost (nothing from infinity on)
           const float y = __fsub_rn((a0 + b0) + (a1 + b1), lost), z = __fadd_rn(sum, y);
-          lost = __fsub_rn(__fsub_rn(z, sum), y);
+          lost = fabsf(z) < INFINITY ? __fsub_rn(__fsub_rn(z, sum), y) : 0.f;
           sum = z;
         }
         turn ^= 1;

@@ -448,7 +448,9 @@ size_t qsa_attention_mass_workspace_size(const qsa_dims *dims, int32_t S, int32_
  *                e^(scale * q_h . K_t - lse_h)
  *   seq_lens, row_start, Nq, q, ws  as in qsa_chunk_attention
  *   lse      fp32 [Nq, Hq]: the rows' LSE (qsa_chunk_attention's lse_out). A
- *            row and head with LSE = -inf gives nothing
+ *            row and head with LSE = -inf gives nothing, one with LSE = NaN
+ *            makes the blocks NaN that it sees; weights past 2^127 may be
+ *            infinite, and are from 2^128 on
  *   mass_in  fp32 [S, ld_mass] or NULL (zeros);  mass  fp32 [S, ld_mass], may
  *            be mass_in itself. All ld_mass entries of the S rows are written
  *            (mass_in's value where no row sees a token of the block).

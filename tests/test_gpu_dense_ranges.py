@@ -222,6 +222,41 @@ def test_weights_of_other_lse():
     assert bool(((weigh(pc, start, q, mine)[0].double() - want).abs() <= 1e-3 * want).all())
 
 
+@pytest.mark.parametrize("Hq,Hkv,L,T", [(8, 2, 200, 70), (8, 1, 140, 40), (4, 4, 300, 260)])
+def test_weights_past_the_range(Hq, Hkv, L, T):
+    """An LSE of NaN makes the blocks NaN that its row sees, and weights past
+    fp32's range make them infinite, whichever column of the products the row and
+    head are and whatever is added afterwards; the other blocks keep their bits."""
+    pc = Paged([L], Hq, Hkv, 64, seed=16)
+    start, q = pc.rows([T], 17)
+    lse = attend(pc, start, q).lse
+    clean = weigh(pc, start, q, lse)[0]
+    for i in range(0, T, 1 if T < 100 else 13):
+        sees = (L - T + i) // 4 + 1  # blocks
+        for h in range(Hq):
+            for value in (math.nan, -500.0):
+                mine = lse.clone()
+                mine[i, h] = value
+                got = weigh(pc, start, q, mine)[0]
+                hit = got.isnan() if math.isnan(value) else got == math.inf
+                assert bool(hit[:sees].all()), (i, h, value)
+                assert torch.equal(got[sees:], clean[sees:])
+
+
+def test_largest_weights():
+    """One weight of 2^126.5 (finite) and of 2^128.5 (not) in any column."""
+    pc = Paged([1], 8, 1, 64, seed=17)
+    start = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    q = torch.zeros((1, 8, 128), dtype=torch.bfloat16, device=DEV)
+    for h in range(8):
+        for e in (126.5, 128.5):
+            lse = torch.full((1, 8), math.inf, device=DEV)
+            lse[0, h] = -e * math.log(2.0)
+            got = float(weigh(pc, start, q, lse)[0, 0])
+            # the LSE is rounded to steps of 2^-17, and so is the exponent
+            assert got == math.inf if e > 128 else abs(got / 2.0 ** e - 1) <= 2.0 ** -15
+
+
 def test_queries_of_others_do_not_matter():
     """NaN and infinity in the rows of other chunks and behind the last one reach
     neither a row's result nor its sequence's weights."""
