@@ -596,8 +596,9 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           x.whole = x.a == 0 && x.b == x.steps;
           at = first + x.b;
         }
+        // (for as long as an item takes: Hkv x up to 4,096 query blocks)
         if (!wait_bar(smem_u32(&ctl.iempty[slot]), (uint32_t)((i / AM_ITEMS) & 1) ^ 1u, abort_flag,
-                      p.err))
+                      p.err, PT_LONG_ROUNDS))
           break;
         ctl.item[slot] = x;
         mbar_arrive(smem_u32(&ctl.ifull[slot]));

@@ -148,6 +148,29 @@ def test_mass_far_before_the_chunk(L, Hq):
         assert abs(float(m.mass[0, j]) - want) <= 2.0 ** -17 * want
 
 
+def test_mass_of_long_items():
+    """Items of 196,608 steps (48 KV heads x 4,096 query blocks), several in each
+    block of the grid: longer than any wait for one step may last. The queries are
+    zero, so a row's weights are 1 / (the tokens it sees). Tolerance as above."""
+    P, L, T, Hkv = 1024, 3 * 2 ** 16, 65535, 48
+    Hq = 8 * Hkv
+    pc = Paged([P], Hq, Hkv, P, seed=24)
+    table = pc.cache.block_table[:1, :1].expand(1, L // P).contiguous()
+    cache = dataclasses.replace(pc.cache, block_table=table)
+    q = torch.zeros((T, Hq, 128), dtype=torch.bfloat16, device=DEV)
+    sees = torch.arange(L - T + 1, L + 1, dtype=torch.float64, device=DEV)
+    lse = sees.log().float()[:, None].expand(T, Hq).contiguous()
+    m = qsa.alloc_attention_mass(pc.dims, 1, T, L // 4)
+    qsa.qsa_attention_mass(pc.dims, cache, torch.tensor([L], dtype=torch.int32, device=DEV),
+                           torch.tensor([0, T], dtype=torch.int32, device=DEV), q, lse, None,
+                           m.mass, m.ws)
+    assert qsa.qsa_check_device_errors() == 0
+    # token t is seen by the rows that see more than t tokens
+    rest = (1 / sees).flip(0).cumsum(0).flip(0)
+    want = Hq * torch.cat((rest[:1].expand(L - T + 1), rest[1:])).view(-1, 4).sum(1)
+    assert bool(((m.mass[0].double() - want).abs() <= 2.0 ** -17 * want).all())
+
+
 def test_mass_without_rows():
     """No rows at all: mass is mass_in (or zeros, or itself), and a chunk that
     reaches past the rows is still flagged."""
