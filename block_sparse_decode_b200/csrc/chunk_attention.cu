@@ -78,6 +78,7 @@ constexpr int CA_PLAN_THREADS = 1024;
 // 254 and 253 with 2, 3, 4 and 6. (With fewer, every CTA gets a step or two: a
 // single sequence's time is latency.)
 constexpr int CA_START = 3, CA_MANY = 16;
+constexpr int CA_MAX_UNITS = 1 << 30;  // units of a CTA (about 20 minutes of work)
 // Chunk tokens that are loaded one by one into a tile that begins as zeros: MMA
 // rows of zeros draw less power than other tokens' (the part throttles at 1 kW)
 constexpr int CA_FEW = 4;
@@ -201,6 +202,11 @@ __global__ void __launch_bounds__(CA_PLAN_THREADS) ca_plan_kernel(CaArgs a, int 
       else a.gpre[g] = off;
     }
     tbase += tot;
+  }
+  // a range of the units counts in 32 bits (CaWalk; an item has 2^24 at most)
+  if (tbase / ctas >= CA_MAX_UNITS) {
+    if (tid == 0) raise_err(a.err, ERR_LEN);
+    tbase = 0;
   }
   if (tid == 0) {
     (G <= CA_PLAN_THREADS ? pre_s : a.gpre)[G] = tbase;

@@ -428,7 +428,9 @@ size_t qsa_chunk_attention_workspace_size(const qsa_dims *dims, int32_t S, int32
  *            calls that may run at the same time need two).
  * Rows outside every chunk stay as they were. So do the rows of a chunk that
  * overruns Nq, is longer than its sequence, or whose sequence is longer than
- * max_pages_per_seq * P (or 2^30) tokens; it raises device error flag 16. A page id out
+ * max_pages_per_seq * P (or 2^30) tokens; it raises device error flag 16. So
+ * does a call of 2^30 and more units per SM, which writes nothing: a unit is
+ * 128 / G rows (G = Hq / Hkv) of a KV head against 128 tokens. A page id out
  * of range raises flag 2 and leaves the values of its sequence's rows
  * undefined. The cache slots past L_s may hold anything; the K and V of
  * tokens below L_s must be finite. A row and head with a score (fp32) that is

@@ -148,6 +148,24 @@ def test_mass_far_before_the_chunk(L, Hq):
         assert abs(float(m.mass[0, j]) - want) <= 2.0 ** -17 * want
 
 
+def test_more_work_than_a_block_can_count():
+    """65,535 rows of 16 KV heads over 2^30 tokens: past 2^30 units of work per block
+    of the grid (5 * 10^11 over some 150), so the call is flagged and writes nothing."""
+    P, L, T = 1024, 2 ** 30, 65535
+    pc = Paged([P], 128, 16, P, seed=25)
+    table = pc.cache.block_table[:1, :1].expand(1, L // P).contiguous()
+    cache = dataclasses.replace(pc.cache, block_table=table)
+    q = torch.zeros((T, 128, 128), dtype=torch.bfloat16, device=DEV)
+    b = qsa.alloc_chunk_attention(pc.dims, 1, T)
+    b.out.fill_(5.0), b.lse.fill_(5.0), b.ws.zero_()
+    qsa.qsa_chunk_attention(pc.dims, cache, torch.tensor([L], dtype=torch.int32, device=DEV),
+                            torch.tensor([0, T], dtype=torch.int32, device=DEV), q, b.out, b.lse,
+                            b.ws)
+    with pytest.raises(qsa.QsaError, match="flags=16"):
+        qsa.qsa_check_device_errors()
+    assert bool((b.out == 5).all()) and bool((b.lse == 5).all())
+
+
 def test_mass_of_long_items():
     """Items of 262,144 steps (64 KV heads x 4,096 query blocks; 0.36 s), several in
     each block of the grid: longer than any wait for one step may last. The queries
