@@ -123,10 +123,10 @@ def _check(status: int):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -495,12 +495,25 @@ def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda"
     return torch.cat((a.cos(), a.sin()), 1).to(torch.float32)
 
 
-def _on_current_device(t, stream):
-    """The calls launch on the current device (or on the device of an explicit
-    stream, which the caller has made current)."""
-    if stream is None and t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _on_current_device(*tensors):
+    """The calls launch on the current device, which is that of an explicit stream
+    too: a kernel cannot read the memory of another one. Returns its index."""
+    current = None
+    for t in tensors:
+        device = -1 if t is None else t.get_device()  # (-1: on the host, refused by _ptr)
+        if device >= 0:
+            if current is None:
+                current = torch.cuda.current_device()
+            if device != current:
+                raise ValueError(f"a tensor is on cuda:{device}, the current device is "
+                                 f"cuda:{current}")
+    return current
+
+
+def _on_cache_device(cache, *tensors):
+    if cache is not None:
+        tensors += (cache.k_pool, cache.v_pool, cache.block_table)
+    return _on_current_device(*tensors)
 
 
 def _head_rows(t: torch.Tensor, name: str):
@@ -521,7 +534,7 @@ def qsa_qk_norm_rope(pos, q, k, q_weight, k_weight, eps: float, rope, q_out, k_o
     q_out, k_out. q and k may be views with any token stride; q_weight /
     k_weight None: no norm; rope (see rope_table) None: no rotation."""
     N, Hq, D = (int(x) for x in q.shape)
-    _on_current_device(q, stream)
+    device = _on_current_device(pos, q, k, q_weight, k_weight, rope, q_out, k_out)
     qp, qs = _head_rows(q, "q")
     kp, ks, Hk = None, 0, 0
     if k is not None:
@@ -542,7 +555,7 @@ def qsa_qk_norm_rope(pos, q, k, q_weight, k_weight, eps: float, rope, q_out, k_o
         float(eps), _ptr(rope, torch.float32, "rope"), 0 if rope is None else int(rope.shape[0]),
         0 if rope is None else int(rope.shape[1]), 1 if interleaved else 0,
         _ptr(q_out, torch.bfloat16, "q_out"),
-        _ptr(k_out, torch.bfloat16, "k_out") if Hk else None, _stream(stream)))
+        _ptr(k_out, torch.bfloat16, "k_out") if Hk else None, _stream(stream, device)))
 
 
 def _shape(t, shape, name):
@@ -566,7 +579,7 @@ def qsa_chunk_attention(dims: QsaDims, cache: QsaCache, seq_lens, row_start, q, 
                         ws=None, stream=None):
     """Dense causal attention of the chunk rows: q [Nq, Hq, D] -> out, lse [Nq, Hq]."""
     S, Nq = _chunk_shapes(dims, seq_lens, row_start, q)
-    _on_current_device(q, stream)
+    device = _on_cache_device(cache, seq_lens, row_start, q, out, lse, ws)
     _shape(out, (Nq, dims.Hq, dims.D), "out")
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out must be bf16 or fp32")
@@ -577,7 +590,7 @@ def qsa_chunk_attention(dims: QsaDims, cache: QsaCache, seq_lens, row_start, q, 
         _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(row_start, torch.int32, "row_start"), Nq,
         _ptr(q, torch.bfloat16, "q"), _ptr(out, None, "out"),
         1 if out.dtype == torch.bfloat16 else 0, _ptr(lse, torch.float32, "lse"),
-        _ptr(ws, None, "ws"), _nbytes(ws), _stream(stream)))
+        _ptr(ws, None, "ws"), _nbytes(ws), _stream(stream, device)))
 
 
 @dataclass
@@ -607,7 +620,7 @@ def qsa_attention_mass(dims: QsaDims, cache: QsaCache, seq_lens, row_start, q, l
     """mass [S, ld] = mass_in (None: 0) + the weight each micro-block got from
     the chunk rows q [Nq, Hq, D] with their lse [Nq, Hq]."""
     S, Nq = _chunk_shapes(dims, seq_lens, row_start, q)
-    _on_current_device(q, stream)
+    device = _on_cache_device(cache, seq_lens, row_start, q, lse, mass_in, mass, ws)
     _shape(lse, (Nq, dims.Hq), "lse")
     ld = int(mass.shape[1])
     _shape(mass, (S, ld), "mass")
@@ -618,7 +631,7 @@ def qsa_attention_mass(dims: QsaDims, cache: QsaCache, seq_lens, row_start, q, l
         _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(row_start, torch.int32, "row_start"), Nq,
         _ptr(q, torch.bfloat16, "q"), _ptr(lse, torch.float32, "lse"),
         _ptr(mass_in, torch.float32, "mass_in"), _ptr(mass, torch.float32, "mass"), ld,
-        _ptr(ws, None, "ws"), _nbytes(ws), _stream(stream)))
+        _ptr(ws, None, "ws"), _nbytes(ws), _stream(stream, device)))
 
 
 @dataclass
@@ -644,7 +657,8 @@ def qsa_evict(dims: QsaDims, cache: QsaCache, seq_lens, mass, keep: int, sink: i
     """Keep `keep` micro-blocks of every sequence (the first `sink`, the last
     `recent`, and the heaviest of the others), copied to dst_table's pages."""
     B, ld = int(seq_lens.shape[0]), int(mass.shape[1])
-    _on_current_device(mass, stream)
+    device = _on_cache_device(cache, seq_lens, mass, dst_table, kept, new_lens, mass_out, ws,
+                              cache.kidx_pool, cache.side_pool)
     _shape(mass, (B, ld), "mass")
     _shape(mass_out, (B, ld), "mass_out")
     _shape(kept, (B, int(keep)), "kept")
@@ -656,7 +670,7 @@ def qsa_evict(dims: QsaDims, cache: QsaCache, seq_lens, mass, keep: int, sink: i
         int(sink), int(recent), _ptr(dst_table, torch.int32, "dst_table"),
         _ptr(kept, torch.int32, "kept"), _ptr(new_lens, torch.int32, "new_lens"),
         _ptr(mass_out, torch.float32, "mass_out"), _ptr(ws, None, "ws"), _nbytes(ws),
-        _stream(stream)))
+        _stream(stream, device)))
 
 
 @dataclass

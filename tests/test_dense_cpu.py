@@ -174,3 +174,51 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="q must have"):
         qsa.qsa_attention_mass(d, None, torch.zeros(2, dtype=torch.int32),
                                torch.zeros(3, dtype=torch.int32), q, None, None, None)
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on device 1."""
+
+    def get_device(self):
+        return 1
+
+
+def _calls():
+    i32, bf = torch.int32, torch.bfloat16
+    d = qsa.QsaDims(8, 2, 128, 4, 64, 16, 0.1)
+    z = torch.zeros
+    pools = dict(k_pool=z((4, 16, 2, 128), dtype=bf), v_pool=z((4, 16, 2, 128), dtype=bf),
+                 kidx_pool=z((4, 16, 64), dtype=bf), side_pool=z((4, 4, 64), dtype=bf),
+                 block_table=z((2, 4), dtype=i32))
+    rows = dict(seq_lens=z(2, dtype=i32), row_start=z(3, dtype=i32), q=z((5, 8, 128), dtype=bf))
+    ws = z(16, dtype=torch.uint8)
+    return {
+        "norm": (lambda a: qsa.qsa_qk_norm_rope(eps=0.0, **a),
+                 dict(pos=z(5, dtype=i32), q=z((5, 8, 128), dtype=bf), k=z((5, 2, 128), dtype=bf),
+                      q_weight=z(128), k_weight=z(128), rope=z((9, 64)),
+                      q_out=z((5, 8, 128), dtype=bf), k_out=z((5, 2, 128), dtype=bf)), ()),
+        "attend": (lambda a, c: qsa.qsa_chunk_attention(d, c, **a),
+                   dict(rows, out=z((5, 8, 128)), lse=z((5, 8)), ws=ws), pools),
+        "mass": (lambda a, c: qsa.qsa_attention_mass(d, c, **a),
+                 dict(rows, lse=z((5, 8)), mass_in=z((2, 7)), mass=z((2, 7)), ws=ws), pools),
+        "evict": (lambda a, c: qsa.qsa_evict(d, c, keep=3, sink=1, recent=1, **a),
+                  dict(seq_lens=z(2, dtype=i32), mass=z((2, 7)), dst_table=z((2, 4), dtype=i32),
+                       kept=z((2, 3), dtype=i32), new_lens=z(2, dtype=i32), mass_out=z((2, 7)),
+                       ws=ws), pools),
+    }
+
+
+@pytest.mark.parametrize("op", ["norm", "attend", "mass", "evict"])
+@pytest.mark.parametrize("stream", [None, 0])
+def test_every_tensor_has_to_be_on_the_current_device(monkeypatch, op, stream):
+    """Any one tensor of another device, pools and scratch among them: refused
+    before anything is launched, on an explicit stream too."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    call, args, pools = _calls()[op]
+    skip = () if op == "evict" else ("kidx_pool", "side_pool")  # (not read by the others)
+    for name in [*args, *(n for n in pools if n not in skip)]:
+        a, p = dict(args, stream=stream), dict(pools)
+        where = a if name in a else p
+        where[name] = where[name].as_subclass(Elsewhere)
+        with pytest.raises(ValueError, match="current device"):
+            call(a, qsa.QsaCache(**p)) if p else call(a)
