@@ -12,7 +12,8 @@
 //   attend  one CTA per SM over an equal range of the flattened steps, so that
 //           one long sequence and many short ones fill the machine alike. An
 //           item that several CTAs share leaves partial results in the
-//           workspace;
+//           workspace. A long range of steps is done in parts of 1,024, which
+//           are added up there;
 //   join    merges those by their LSEs.
 //
 // attend: the G query heads of a KV head share its K and V, so a tile of 128
@@ -82,6 +83,13 @@ constexpr int CA_MAX_UNITS = 1 << 30;  // units of a CTA (about 20 minutes of wo
 // Chunk tokens that are loaded one by one into a tile that begins as zeros: MMA
 // rows of zeros draw less power than other tokens' (the part throttles at 1 kW)
 constexpr int CA_FEW = 4;
+// Steps after which O leaves the tensor memory: the tensor cores' additions to it
+// truncate, a bias of up to 2^-23 of the sum each, 8 a step. Parts of 1,024 steps
+// (131,072 tokens) keep that below 2^-10 of sum w |V|. Measured with equal scores
+// and positive V in one item of 2^26 tokens: 19% off without parts, 0.01% with them
+// (2^28: 51%, 0.012%), at 2% of the time. What the parts add up to is fp32,
+// rounded to nearest.
+constexpr int CA_PART = 1024;
 constexpr float CA_LAZY = 8.f;  // growth of the maximum that is left in the sums
 
 struct CaArgs {
@@ -93,6 +101,7 @@ struct CaArgs {
   int4 *ginfo;       // [2 Gmax] {seq, first row, tokens, steps}, {tokens its first row sees, L, -, -}
   float *rec_lse;    // [CTAs][2][2][128]
   float *rec_o;      // [CTAs][2][2][128][128]
+  float2 *part;      // [CTAs][2][2][128] sum and maximum (log2) of an item's parts so far
   void *out;
   float *lse;
   PagedTiles pages;
@@ -262,7 +271,7 @@ struct CaWalk {
   int g, h, w, start;
   int4 gi;  // {seq, first row, tokens, steps}
   int lim0, L;
-  int a, b;  // this CTA's steps of the item
+  int a = 0, b = 0;  // this CTA's steps of the item
   const CaArgs &p;
 
   __device__ CaWalk(const CaArgs &args, int c) : p(args) {
@@ -305,13 +314,14 @@ struct CaWalk {
   }
 };
 
-// An item as the roles see it: this CTA's steps [a, b), none at the end of the
-// range. Slot 0's rows of a two-tile item see its steps below n0; a one-tile
+// An item as the roles see it: this CTA's steps [a, b), or a part of them (of
+// CA_PART, the last one of 2 to CA_PART + 1, so that both slots have a step of
+// every part but a CTA's first), none at the end of the range. Slot 0's rows of a two-tile item see its steps below n0; a one-tile
 // item (n0 = -1) has its steps in turn on slot 0 and slot 1.
 struct __align__(16) CaItem {
   int a, b, n0, ntok;
-  int h, row0, lim0, whole;
-  int seq, L, pad0, pad1;
+  int h, row0, lim0, whole;  // whole: the result is final, else a record
+  int seq, L, part, rec;     // part: 1 adds to the parts before, 2 more follow; rec: which record
   __device__ bool two() const { return n0 >= 0; }
 };
 __device__ __forceinline__ bool ca_active(int s, int j, int a, int n0) {
@@ -622,8 +632,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         any = true;
       }
       if (!ok) break;
-      const size_t rec =
-          ((size_t)blockIdx.x * 2 + (it.a == 0 ? 1 : 0)) * 256 + s * 128 + r;
+      const size_t rec = ((size_t)blockIdx.x * 2 + it.rec) * 256 + s * 128 + r;
       if (!any) {  // slot 0's rows see none of this CTA's steps of a two-tile item
         if (it.two() && valid && half == 0) p.rec_lse[rec] = -INFINITY;
         continue;
@@ -663,14 +672,24 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       if (ok && live) {
         // (a sum of 0: nothing seen, or no weight above 0 here. One that is NaN,
         // from a score that is NaN or +inf, goes on to the result and its LSE)
-        const float M = fmaxf(l != 0.f ? m : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
+        // (the parts before: this thread's own record, not yet divided by its sum)
+        const bool adds = (it.part & 1) && valid, more = (it.part & 2) != 0;
+        const size_t mine = ((size_t)blockIdx.x * 4 + s * 2 + half) * 128 + r;
+        float2 old = make_float2(0.f, -INFINITY);
+        if (adds) old = p.part[mine];
+        const float M = fmaxf(fmaxf(l != 0.f ? m : -INFINITY, l1 != 0.f ? m1 : -INFINITY),
+                              old.x != 0.f ? old.y : -INFINITY);
         const float e0 = l != 0.f ? ex2_approx(m - M) : 0.f;
         const float e1 = l1 != 0.f ? ex2_approx(m1 - M) : 0.f;
-        const float sum = e0 * l + e1 * l1;
-        const float f0 = sum != 0.f ? e0 / sum : 0.f, f1 = sum != 0.f ? e1 / sum : 0.f;
+        const float e2 = old.x != 0.f ? ex2_approx(old.y - M) : 0.f;
+        const float sum = e0 * l + e1 * l1 + e2 * old.x;
+        const float div = more ? 1.f : sum;
+        const float f0 = sum != 0.f ? e0 / div : 0.f, f1 = sum != 0.f ? e1 / div : 0.f;
+        const float f2 = sum != 0.f ? e2 / div : 0.f;
         const bool whole = it.whole != 0;
+        if (more && valid) p.part[mine] = make_float2(sum, M);
         const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
-        if (valid && half == 0) {
+        if (valid && half == 0 && !more) {
           const float lse = sum != 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           if (!whole) p.rec_lse[rec] = lse;
           else if (p.lse != nullptr) p.lse[row] = lse;
@@ -697,6 +716,17 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           }
           if (!valid) continue;
           const int col = half * 64 + 32 * c;
+          if (adds && f2 != 0.f) {
+            const float4 *d = reinterpret_cast<const float4 *>(p.rec_o + rec * CA_D + col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = d[i];
+              o[4 * i] = fmaf(v.x, f2, o[4 * i]);
+              o[4 * i + 1] = fmaf(v.y, f2, o[4 * i + 1]);
+              o[4 * i + 2] = fmaf(v.z, f2, o[4 * i + 2]);
+              o[4 * i + 3] = fmaf(v.w, f2, o[4 * i + 3]);
+            }
+          }
           if (whole && p.out_bf16) {
             uint4 *d =
                 reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D + col);
@@ -948,22 +978,27 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       if (lane == 0) {
         CaWalk w(p, blockIdx.x);
         bool more = w.next(true);
+        int from = w.a;  // the next part's first step
         for (int at = 0;; ++at) {
           const int i = at % CA_ITEMS;
           if (!wait_bar(smem_u32(&ctl.iempty[i]), (uint32_t)((at / CA_ITEMS) & 1) ^ 1u, abort_flag,
-                        p.err, PT_LONG_ROUNDS))
+                        p.err))
             break;
           CaItem &it = ctl.item[i];
           it.a = it.b = 0;
+          int to = 0;
           if (more) {
-            it.a = w.a;
-            it.b = w.b;
+            to = w.b - from <= CA_PART + 1 ? w.b : from + CA_PART;
+            it.a = from;
+            it.b = to;
+            it.part = (from > w.a ? 1 : 0) | (to < w.b ? 2 : 0);
+            it.rec = w.a == 0 ? 1 : 0;
             it.n0 = w.w == 2 ? (w.lim0 + p.TT - 1 + CA_KT - 1) / CA_KT : -1;
             it.ntok = w.gi.z;
             it.h = w.h;
             it.row0 = w.gi.y;
             it.lim0 = w.lim0;
-            it.whole = w.a == 0 && w.b == w.gi.w;
+            it.whole = w.a == 0 && to == w.gi.w;
             it.seq = w.gi.x;
             it.L = w.L;
           }
@@ -971,9 +1006,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
           if (!more) break;
           // the item's query tiles, once the one before it has used its own
           // (its K and V tiles are on their way already)
-          if (at > 0 &&
-              !wait_bar(qempty, (uint32_t)(at - 1) & 1u, abort_flag, p.err, PT_LONG_ROUNDS))
-            break;
+          if (at > 0 && !wait_bar(qempty, (uint32_t)(at - 1) & 1u, abort_flag, p.err)) break;
           const int tiles = w.w == 2 ? 2 : 1;
           if (w.gi.z <= CA_FEW) {  // one by one: the tile's other rows stay zero
             mbar_arrive_expect(qfull, (uint32_t)(w.gi.z * p.G * 256));
@@ -989,7 +1022,11 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
                             w.gi.y + s * p.TT);
           }
           ctl.qissued = at + 1;
-          more = w.next(false);
+          from = to;
+          if (to == w.b) {
+            more = w.next(false);
+            from = w.a;
+          }
         }
       }
       __syncwarp();
@@ -1073,7 +1110,7 @@ __global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
 // ------------------------------------------------------------------ host
 
 struct CaLayout {
-  size_t first, shared, gpre, ginfo, lse, o, bytes;
+  size_t first, shared, gpre, ginfo, lse, o, part, bytes;
   int Gmax, TT, ctas;
 };
 
@@ -1089,7 +1126,8 @@ CaLayout ca_layout(const qsa_dims &d, int S, int Nq) {
   l.ginfo = l.gpre + r(8 * ((size_t)l.Gmax + 1));
   l.lse = l.ginfo + r(32 * (size_t)l.Gmax);
   l.o = l.lse + r((size_t)l.ctas * 512 * 4);
-  l.bytes = l.o + (size_t)l.ctas * 512 * CA_D * 4;
+  l.part = l.o + (size_t)l.ctas * 512 * CA_D * 4;
+  l.bytes = l.part + (size_t)l.ctas * 512 * 8;
   return l;
 }
 
@@ -1119,6 +1157,7 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   a.ginfo = reinterpret_cast<int4 *>(w + l.ginfo);
   a.rec_lse = reinterpret_cast<float *>(w + l.lse);
   a.rec_o = reinterpret_cast<float *>(w + l.o);
+  a.part = reinterpret_cast<float2 *>(w + l.part);
   a.out = out;
   a.lse = lse;
   a.S = S;

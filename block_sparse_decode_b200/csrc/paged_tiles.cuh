@@ -59,8 +59,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // issue slots from the softmax (ragged chunks 248 us without the pause, 228 with
 // it and no less with a longer one).
 // A round that nothing ends takes 4 us: PT_WAIT_ROUNDS are 0.27 s. A wait for a
-// whole item (up to 2^30 tokens of an attention, 2^23 steps, 18 s) takes
-// PT_LONG_ROUNDS, 34 s; when another role gives up, it ends within a round.
+// whole item of the attention weights (KV heads x up to 4,096 query blocks, 1.4 us
+// each) takes PT_LONG_ROUNDS, 34 s; when another role gives up, it ends within a
+// round.
 constexpr uint32_t PT_WAIT_NS = 20000, PT_WAIT_ROUNDS = 1u << 16, PT_LONG_ROUNDS = 1u << 23;
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                          unsigned *err, uint32_t rounds = PT_WAIT_ROUNDS) {

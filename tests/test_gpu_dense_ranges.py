@@ -148,6 +148,50 @@ def test_mass_far_before_the_chunk(L, Hq):
         assert abs(float(m.mass[0, j]) - want) <= 2.0 ** -17 * want
 
 
+@pytest.mark.parametrize("L,T,S,Hq,flat", [
+    (128 * 1025, 1, 150, 8, True), (128 * 1025 + 1, 1, 300, 8, False), (2 ** 18 + 1, 1, 400, 5, True),
+    (2 ** 18 + 77, 33, 90, 8, False), (128 * 2050 + 9, 32, 200, 8, True), (2 ** 22 + 130, 1, 160, 8, True),
+    (2 ** 22 + 130, 1, 1, 8, False), (2 ** 24 + 3, 20, 10, 6, True), (2 ** 26, 1, 160, 8, True)])
+def test_long_sums(L, T, S, Hq, flat):
+    """Items of many steps, whole and shared, of one and of two tiles: results and
+    LSEs as exact as those of short ones. The values are positive, so that what
+    the additions lose adds up too; every page of a sequence is the same one.
+    A part of 1,024 steps makes up to 8 * 1,025 additions in the tensor cores, off
+    by at most 2^-23 of the sum each: 2^-10 + 2^-12 in all, next to the bound that
+    every result has. With equal scores (flat) every weight is 1 and none is
+    rounded. The row sums add 2^10 values a part and up to 2^9 parts in fp32,
+    2^-24 each: 2^-13; and the LSE is held to 2^-20."""
+    P = 1024
+    pc = Paged([P], Hq, 1, P, seed=26)
+    pc.v[0] = pc.v[0].abs() + 0.25
+    page, slot = pc.places(pc.cache.block_table, 0, P, P)
+    pc.cache.v_pool[page, slot] = pc.v[0]
+    pages = -(-L // P)
+    table = pc.cache.block_table[:1, :1].expand(S, pages).contiguous()
+    cache = dataclasses.replace(pc.cache, block_table=table)
+    q = randn((S * T, Hq, 128), 18) * (0.0 if flat else 1.0)
+    start = torch.arange(S + 1, dtype=torch.int32, device=DEV) * T
+    lens = torch.full((S,), L, dtype=torch.int32, device=DEV)
+    b = qsa.alloc_chunk_attention(pc.dims, S, S * T, out_dtype=torch.float32)
+    b.ws.random_(0, 255)
+    qsa.qsa_chunk_attention(pc.dims, cache, lens, start, q, b.out, b.lse, b.ws)
+    assert qsa.qsa_check_device_errors() == 0
+    # how often a row sees each token of the page
+    sees = (L - T + 1 + torch.arange(T, device=DEV)).repeat(S)
+    n = (sees[:, None] - torch.arange(P, device=DEV) + P - 1) // P
+    z = torch.einsum("rhd,td->rht", q.double(), pc.k[0][:, 0].double()) * pc.dims.scale
+    z = z + n.double().log()[:, None]
+    lse = torch.logsumexp(z, -1)
+    ref = torch.einsum("rht,td->rhd", torch.exp(z - lse[..., None]), pc.v[0][:, 0].double())
+    bound = 2.0 ** -10 + 2.0 ** -12 + (0.0 if flat else HALF + 2.0 ** -12)
+    assert bool(((b.out.double() - ref).abs() <= bound * ref).all())
+    bound = 2.0 ** -13 + 2.0 ** -19 + (0.0 if flat else 1e-3)
+    assert float((b.lse.double() - lse).abs().max()) <= bound
+    again = qsa.alloc_chunk_attention(pc.dims, S, S * T, out_dtype=torch.bfloat16)
+    qsa.qsa_chunk_attention(pc.dims, cache, lens, start, q, again.out, again.lse, b.ws)
+    assert torch.equal(again.out, b.out.to(torch.bfloat16)) and torch.equal(again.lse, b.lse)
+
+
 def test_more_work_than_a_block_can_count():
     """65,535 rows of 16 KV heads over 2^30 tokens: past 2^30 units of work per block
     of the grid (5 * 10^11 over some 150), so the call is flagged and writes nothing."""
