@@ -68,6 +68,7 @@ struct AmArgs {
   long long *base;  // [S + 1] prefix of the sequences' steps
   float *rec;       // [CTAs][2][64] partial sums of shared items
   int S, Nq, Hq, Hkv, G, TT, ld;
+  int k_tiles;      // failure injection: pairs of K tiles that a CTA issues
   float c2;         // scale * log2(e)
   unsigned *err;
 };
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
       t0.step(p.pages);
       const int sl1 = t0.slot, p1 = t0.take(p.pages);
       for (int h = it.a / it.nq; h <= (it.b - 1) / it.nq; ++h) {
-        ok = wait_all(kempty + 8 * kb, kph, abort_flag, p.err);
+        ok = wait_all(kempty + 8 * kb, kph, abort_flag, p.err) && cnt != p.k_tiles;
         if (!ok) break;
         const unsigned l0 = __ballot_sync(0xffffffffu, p0 >= 0);
         const unsigned l1 = __ballot_sync(0xffffffffu, p1 >= 0);
@@ -700,6 +701,7 @@ cudaError_t launch_attention_mass(const qsa_dims &d, const qsa_cache &c, int S,
   a.G = d.Hq / d.Hkv;
   a.TT = 128 / a.G;
   a.ld = ld;
+  a.k_tiles = debug_stall_dense();
   a.c2 = d.scale * 1.4426950408889634f;
   a.err = err;
   // the copy of mass_in (none where it is mass itself), 16 KB a block

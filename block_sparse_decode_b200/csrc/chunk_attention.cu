@@ -54,6 +54,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "launch.h"
@@ -106,6 +107,7 @@ struct CaArgs {
   float *lse;
   PagedTiles pages;
   int S, Nq, Gmax, Hq, Hkv, G, TT, out_bf16;
+  int k_tiles;  // failure injection: K tiles that a CTA issues (debug_stall_dense())
   float scale;
   unsigned *err;
 };
@@ -915,12 +917,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       PagePieces pieces;
       const bool lead = elect_one();
       CaPlace kt;
+      int left = p.k_tiles;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
         pieces.start(p.pages, it.seq, it.L, it.a, lane);
         for (int j = it.a; j < it.b; ++j) {
           const int page = pieces.take(p.pages);
-          ok = wait_all(empty0 + 8 * kt.st, kt.ph ^ 1u, abort_flag, p.err);
+          ok = wait_all(empty0 + 8 * kt.st, kt.ph ^ 1u, abort_flag, p.err) && left-- != 0;
           if (!ok) break;
           load_tile(p.pages, &k_map, ring + kt.st * PT_TILE, full0 + 8 * kt.st, page, pieces.slot,
                     it.h, lead);
@@ -1133,6 +1136,11 @@ CaLayout ca_layout(const qsa_dims &d, int S, int Nq) {
 
 }  // namespace
 
+int debug_stall_dense() {
+  const char *e = getenv("QSA_DEBUG_STALL_DENSE");
+  return e != nullptr ? atoi(e) : -1;
+}
+
 size_t chunk_attention_ws_bytes(const qsa_dims &d, int S, int Nq) {
   return ca_layout(d, S, Nq).bytes;
 }
@@ -1170,6 +1178,7 @@ cudaError_t launch_chunk_attention(const qsa_dims &d, const qsa_cache &c, int S,
   a.pages = paged_tiles(d, c, err);
   a.out_bf16 = out_is_bf16;
   a.scale = d.scale;
+  a.k_tiles = debug_stall_dense();
   a.err = err;
 
   CUtensorMap q_map, q1_map, k_map, v_map;

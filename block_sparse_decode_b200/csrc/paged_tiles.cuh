@@ -200,6 +200,13 @@ __device__ __forceinline__ void load_tile(const PagedTiles &p, const CUtensorMap
   issue_tile(p, map, dst, bar, page, slot, h, lead);
 }
 
+// Failure injection for the two kernels that stream the cache through these tiles,
+// read at each launch from the environment variable QSA_DEBUG_STALL_DENSE: a CTA
+// issues that many K tiles (pairs of them, for the attention weights) and then no
+// more, as if a copy had been lost, and every role's waits run out (after 0.27 s).
+// -1 where it is unset: no limit.
+int debug_stall_dense();
+
 inline PagedTiles paged_tiles(const qsa_dims &d, const qsa_cache &c, unsigned *err) {
   PagedTiles t;
   t.table = c.block_table;
