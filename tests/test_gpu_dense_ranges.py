@@ -210,6 +210,32 @@ def test_more_work_than_a_block_can_count():
     assert bool((b.out == 5).all()) and bool((b.lse == 5).all())
 
 
+@pytest.mark.parametrize("lens,chunks,Hq,Hkv,P", [
+    ([4099, 1500], [1, 1], 8, 2, 64), ([1000, 33, 257], [17, 16, 257], 32, 4, 48),
+    ([700], [129], 21, 3, 4), ([5000], [1300], 8, 1, 64), ([30000, 7], [40, 7], 6, 1, 128)])
+def test_mass_to_fp32(lens, chunks, Hq, Hkv, P):
+    """Queries of -1, 0, 1 and keys of whole numbers up to 2: every score is exact, so
+    what is left is the fp32 arithmetic on it. In the exponent of a weight, in
+    units of log2 with scores below 8 and LSEs below 16: log2(e) in both
+    products 2^-21 + 2^-20, the LSE's own rounding 2^-20, the two results' 2^-21
+    + 2^-20, below 2^-18 in all; the exponential 2^-22; 32 columns added up four
+    times in parallel 2^-19, and the rest of the sum 2^-21. Below 2^-17 together,
+    with the sum of positive terms."""
+    pc = Paged(lens, Hq, Hkv, P, seed=27)
+    pc.dims = dataclasses.replace(pc.dims, scale=0.125)
+    start, q = pc.rows(chunks, 19)
+    q = q.clamp(-1, 1).round()
+    for s, n in enumerate(lens):
+        pc.k[s] = pc.k[s].clamp(-2, 2).round()
+        page, slot = pc.places(pc.cache.block_table, s, n, P)
+        pc.cache.k_pool[page, slot] = pc.k[s]
+    _, lse, _, mass = attention_ref(pc, chunks, q)
+    assert float(lse.max()) < 16
+    got = weigh(pc, start, q, lse.float().contiguous())
+    for s, want in enumerate(mass):
+        assert bool(((got[s, :want.numel()].double() - want).abs() <= 2.0 ** -17 * want).all())
+
+
 def test_mass_of_long_items():
     """Items of 262,144 steps (64 KV heads x 4,096 query blocks; 0.36 s), several in
     each block of the grid: longer than any wait for one step may last. The queries
