@@ -422,6 +422,90 @@ struct CaItems {
   }
 };
 
+// The result of an item's row, of this half's columns: the slot's own sum and
+// maximum (l, m), and those of slot 1 (l1, m1) where it had a part of a one-tile
+// item. A sum of 0: nothing seen, or no weight above 0 here; one that is NaN, from
+// a score that is NaN or +inf, goes on to the result and its LSE. With PARTS, what
+// the parts before left (not yet divided by its sum) is in this thread's own record.
+template <bool PARTS>
+__device__ __forceinline__ void ca_finish(const CaArgs &p, const CaItem &it, int s, int half, int r,
+                                          int tok, bool valid, bool has1, float l, float m, float l1,
+                                          float m1) {
+  const int warp = threadIdx.x >> 5;
+  const size_t rec = ((size_t)blockIdx.x * 2 + it.rec) * 256 + s * 128 + r;
+  const bool adds = PARTS && (it.part & 1) && valid, more = PARTS && (it.part & 2) != 0;
+  const size_t mine = ((size_t)blockIdx.x * 4 + s * 2 + half) * 128 + r;
+  float2 old = make_float2(0.f, -INFINITY);
+  if (adds) old = p.part[mine];
+  float M = fmaxf(l != 0.f ? m : -INFINITY, l1 != 0.f ? m1 : -INFINITY);
+  if (PARTS) M = fmaxf(M, old.x != 0.f ? old.y : -INFINITY);
+  const float e0 = l != 0.f ? ex2_approx(m - M) : 0.f;
+  const float e1 = l1 != 0.f ? ex2_approx(m1 - M) : 0.f;
+  const float e2 = adds && old.x != 0.f ? ex2_approx(old.y - M) : 0.f;
+  float sum = e0 * l + e1 * l1;
+  if (PARTS) sum += e2 * old.x;
+  // (e0 to e2 are powers of two: one division gives what three would)
+  const float inv = more ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
+  const float f0 = e0 * inv, f1 = e1 * inv, f2 = e2 * inv;
+  const bool whole = it.whole != 0;
+  if (more && valid) p.part[mine] = make_float2(sum, M);
+  const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
+  if (valid && half == 0 && !more) {
+    const float lse = sum != 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (!whole) p.rec_lse[rec] = lse;
+    else if (p.lse != nullptr) p.lse[row] = lse;
+  }
+  const uint32_t to =
+      (uint32_t)(256 + s * 128 + half * 64) + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    float o[32];
+    tc_ld32_nowait(to + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? o[i] * f0 : 0.f;
+    if (has1) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 16) {
+        float o1[16];
+        tc_ld16(to + 128 + 32 * c + k, o1);
+        if (f1 != 0.f) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[k + i] = fmaf(o1[i], f1, o[k + i]);
+        }
+      }
+    }
+    if (!valid) continue;
+    const int col = half * 64 + 32 * c;
+    if (adds && f2 != 0.f) {
+      const float4 *d = reinterpret_cast<const float4 *>(p.rec_o + rec * CA_D + col);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 v = d[i];
+        o[4 * i] = fmaf(v.x, f2, o[4 * i]);
+        o[4 * i + 1] = fmaf(v.y, f2, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(v.z, f2, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(v.w, f2, o[4 * i + 3]);
+      }
+    }
+    if (whole && p.out_bf16) {
+      uint4 *d =
+          reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        d[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                          pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                          pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+    } else {
+      float4 *d = reinterpret_cast<float4 *>(
+          (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + col);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    }
+  }
+}
 __global__ void __launch_bounds__(CA_THREADS, 1)
     ca_attend_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap q1_map,
@@ -672,80 +756,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
         m1 = ctl.pm[1][1][r];
       }
       if (ok && live) {
-        // (a sum of 0: nothing seen, or no weight above 0 here. One that is NaN,
-        // from a score that is NaN or +inf, goes on to the result and its LSE)
-        // (the parts before: this thread's own record, not yet divided by its sum)
-        const bool adds = (it.part & 1) && valid, more = (it.part & 2) != 0;
-        const size_t mine = ((size_t)blockIdx.x * 4 + s * 2 + half) * 128 + r;
-        float2 old = make_float2(0.f, -INFINITY);
-        if (adds) old = p.part[mine];
-        const float M = fmaxf(fmaxf(l != 0.f ? m : -INFINITY, l1 != 0.f ? m1 : -INFINITY),
-                              old.x != 0.f ? old.y : -INFINITY);
-        const float e0 = l != 0.f ? ex2_approx(m - M) : 0.f;
-        const float e1 = l1 != 0.f ? ex2_approx(m1 - M) : 0.f;
-        const float e2 = old.x != 0.f ? ex2_approx(old.y - M) : 0.f;
-        const float sum = e0 * l + e1 * l1 + e2 * old.x;
-        const float div = more ? 1.f : sum;
-        const float f0 = sum != 0.f ? e0 / div : 0.f, f1 = sum != 0.f ? e1 / div : 0.f;
-        const float f2 = sum != 0.f ? e2 / div : 0.f;
-        const bool whole = it.whole != 0;
-        if (more && valid) p.part[mine] = make_float2(sum, M);
-        const size_t row = (size_t)(it.row0 + tok) * p.Hq + (size_t)it.h * p.G + r % p.G;
-        if (valid && half == 0 && !more) {
-          const float lse = sum != 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-          if (!whole) p.rec_lse[rec] = lse;
-          else if (p.lse != nullptr) p.lse[row] = lse;
-        }
-        const uint32_t to =
-            tmem + (uint32_t)(256 + s * 128 + half * 64) + ((uint32_t)((warp & 3) * 32) << 16);
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          float o[32];
-          tc_ld32_nowait(to + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
-          tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? o[i] * f0 : 0.f;
-          if (has1) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 16) {
-              float o1[16];
-              tc_ld16(to + 128 + 32 * c + k, o1);
-              if (f1 != 0.f) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[k + i] = fmaf(o1[i], f1, o[k + i]);
-              }
-            }
-          }
-          if (!valid) continue;
-          const int col = half * 64 + 32 * c;
-          if (adds && f2 != 0.f) {
-            const float4 *d = reinterpret_cast<const float4 *>(p.rec_o + rec * CA_D + col);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 v = d[i];
-              o[4 * i] = fmaf(v.x, f2, o[4 * i]);
-              o[4 * i + 1] = fmaf(v.y, f2, o[4 * i + 1]);
-              o[4 * i + 2] = fmaf(v.z, f2, o[4 * i + 2]);
-              o[4 * i + 3] = fmaf(v.w, f2, o[4 * i + 3]);
-            }
-          }
-          if (whole && p.out_bf16) {
-            uint4 *d =
-                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row * CA_D + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              d[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
-                                pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
-                                pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-          } else {
-            float4 *d = reinterpret_cast<float4 *>(
-                (whole ? static_cast<float *>(p.out) + row * CA_D : p.rec_o + rec * CA_D) + col);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-        }
+        if (it.part == 0) ca_finish<false>(p, it, s, half, r, tok, valid, has1, l, m, l1, m1);
+        else ca_finish<true>(p, it, s, half, r, tok, valid, has1, l, m, l1, m1);
       }
       tc_fence_before();
       __syncwarp();
@@ -917,13 +929,13 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       PagePieces pieces;
       const bool lead = elect_one();
       CaPlace kt;
-      int left = p.k_tiles;
+      int left = p.k_tiles < 0 ? 0x7fffffff : p.k_tiles;
       bool ok = true;
       while (ok && items.next(ctl, it, p.err)) {
         pieces.start(p.pages, it.seq, it.L, it.a, lane);
         for (int j = it.a; j < it.b; ++j) {
           const int page = pieces.take(p.pages);
-          ok = wait_all(empty0 + 8 * kt.st, kt.ph ^ 1u, abort_flag, p.err) && left-- != 0;
+          ok = wait_all(empty0 + 8 * kt.st, kt.ph ^ 1u, abort_flag, p.err) && --left >= 0;
           if (!ok) break;
           load_tile(p.pages, &k_map, ring + kt.st * PT_TILE, full0 + 8 * kt.st, page, pieces.slot,
                     it.h, lead);
@@ -1071,31 +1083,36 @@ __global__ void __launch_bounds__(256) ca_join_kernel(const CaArgs p) {
   for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += 8 * gridDim.y) {
     const int at = i < per_tile ? i : 128 + i - per_tile;
     auto rec = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * 256 + at; };
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.rec_lse + rec(c)));
+    auto part = [&](int c) { return c <= c1 ? __ldcg(p.rec_lse + rec(c)) : -INFINITY; };
+    const float mine = part(c0 + lane);  // a lane's part of the first 32
+    float M = mine;
+    for (int c = c0 + 32 + lane; c <= c1; c += 32) M = fmaxf(M, part(c));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    // (fmaxf passes over a part whose LSE is NaN; its factor is NaN)
-    for (int c = c0; c <= c1; c += 4) {
-      float f[4];
-      float4 v[4];
+    for (int b0 = c0; b0 <= c1; b0 += 32) {
+      // (fmaxf passed over a part whose LSE is NaN; its factor is NaN)
+      const float e = b0 == c0 ? mine : part(b0 + lane);
+      const float fl = e == -INFINITY ? 0.f : __expf(e - M);
+      for (int c = b0; c <= min(c1, b0 + 31); c += 4) {
+        float f[4];
+        float4 v[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float e = c + u <= c1 ? __ldcg(p.rec_lse + rec(c + u)) : -INFINITY;
-        f[u] = e == -INFINITY ? 0.f : __expf(e - M);
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (f[u] != 0.f)
-          v[u] = __ldcg(reinterpret_cast<const float4 *>(p.rec_o + rec(c + u) * CA_D) + lane);
-      }
+        for (int u = 0; u < 4; ++u) {
+          f[u] = __shfl_sync(0xffffffffu, fl, c - b0 + u);  // (0 past the last part)
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (f[u] != 0.f)
+            v[u] = __ldcg(reinterpret_cast<const float4 *>(p.rec_o + rec(c + u) * CA_D) + lane);
+        }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        sum += f[u];
-        acc.x = fmaf(f[u], v[u].x, acc.x);
-        acc.y = fmaf(f[u], v[u].y, acc.y);
-        acc.z = fmaf(f[u], v[u].z, acc.z);
-        acc.w = fmaf(f[u], v[u].w, acc.w);
+        for (int u = 0; u < 4; ++u) {
+          sum += f[u];
+          acc.x = fmaf(f[u], v[u].x, acc.x);
+          acc.y = fmaf(f[u], v[u].y, acc.y);
+          acc.z = fmaf(f[u], v[u].z, acc.z);
+          acc.w = fmaf(f[u], v[u].w, acc.w);
+        }
       }
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
