@@ -24,9 +24,9 @@
 // query blocks stream past them (each query block from L2 serves 256 tokens,
 // 16 bytes a clock per SM), so prompts are bound by the exponentials: 16 a
 // clock per SM, 2,048 clocks a step of 256 x 128. A quarter of them goes to the
-// fp32 units instead: 8,192 rows of a prompt (32 query heads) 375 us without,
-// 363 with an eighth, 354 with a quarter. One decode token per sequence is
-// bound by reading K once: 180 us for 32 x 32,768 tokens, 6.0 TB/s.
+// fp32 units instead: 8,192 rows of a prompt (32 query heads) 403 us without,
+// 389 with an eighth, 378 with a quarter, 387 with three eighths. One decode token
+// per sequence is bound by reading K once: 182 us for 32 x 32,768 tokens, 5.9 TB/s.
 //   warps 0-7, 8-15 the weights of the even and the odd steps (S^T is double
 //                   buffered), 4 warps for each of the two K tiles
 //   warp 16         issues the MMAs
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           f2_unpack(la, a0, a1);
           f2_unpack(lb, b0, b1);
           // the sum with what its last rounding lost (bounded below: NaN once the
-          // sum is infinite, which then stays so. A selection in its place took
-          // 394 us for the 8,192-row prompt, this 387)
+          // sum is infinite, which then stays so; a selection in the bound's place
+          // is 2% slower)
           const float y = __fsub_rn((a0 + b0) + (a1 + b1), lost), z = __fadd_rn(sum, y);
           lost = fmaxf(__fsub_rn(__fsub_rn(z, sum), y), -3.4028235e38f);
           sum = z;

@@ -487,7 +487,9 @@ size_t qsa_evict_workspace_size(int32_t B, int32_t ld_mass, int32_t keep);
  *             then zeros (not mass itself)
  *   ws        may be NULL when its size is 0.
  * A sequence that is negative or longer than 4 * ld_mass tokens raises device
- * error flag 16 and gets n = 0. Supported: 1 <= ld_mass, keep <= 2^28 (2^30
+ * error flag 16 and gets n = 0. A kept block whose source or destination page id
+ * is out of range raises flag 2, one behind the tables' last column flag 4; it
+ * is not copied, but still listed and counted. Supported: 1 <= ld_mass, keep <= 2^28 (2^30
  * tokens), sink >= 0, recent >= 1, sink + recent <= keep. */
 qsa_status qsa_evict(const qsa_dims *dims, const qsa_cache *cache, int32_t B,
                      const int32_t *seq_lens, const float *mass, int32_t ld_mass, int32_t keep,

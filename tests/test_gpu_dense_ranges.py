@@ -423,6 +423,42 @@ def test_scores_that_are_not_finite(lens, chunks, Hq, Hkv):
     assert float((got.lse[rows, 3].double() - lse[rows, 3]).abs().max()) <= 1e-3
 
 
+def test_scores_that_are_not_finite_in_long_items():
+    """The same where an item is done in parts: a NaN that only the last tokens
+    of the page bring reaches every part, a row of -infinity none."""
+    P, L, S, Hq = 1024, 128 * 2050, 150, 8
+    pc = Paged([P], Hq, 1, P, seed=43)
+    pc.k[0][:, :, 0] = 0
+    pc.k[0][P - 3, :, 0] = 2.0
+    pc.k[0][:, :, 1] = 2.0
+    page, slot = pc.places(pc.cache.block_table, 0, P, P)
+    pc.cache.k_pool[page, slot] = pc.k[0]
+    table = pc.cache.block_table[:1, :1].expand(S, -(-L // P)).contiguous()
+    cache = dataclasses.replace(pc.cache, block_table=table)
+    lens = torch.full((S,), L, dtype=torch.int32, device=DEV)
+    start = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+    q = randn((S, Hq, 128), 20)
+    b = qsa.alloc_chunk_attention(pc.dims, S, S, out_dtype=torch.float32)
+
+    def call():
+        qsa.qsa_chunk_attention(pc.dims, cache, lens, start, q, b.out, b.lse, b.ws)
+        assert qsa.qsa_check_device_errors() == 0
+        return b.out.clone(), b.lse.clone()
+
+    clean = call()
+    q[::3, 0] = math.nan
+    q[::3, 1] = 0
+    q[::3, 1, 0] = 3e38
+    q[::3, 2] = 0
+    q[::3, 2, 1] = -3e38
+    out, lse = call()
+    assert bool(out[::3, :2].isnan().all()) and bool(lse[::3, :2].isnan().all())
+    assert bool((out[::3, 2] == 0).all()) and bool((lse[::3, 2] == -math.inf).all())
+    same = torch.ones((S, Hq), dtype=torch.bool, device=DEV)
+    same[::3, :3] = False
+    assert torch.equal(out[same], clean[0][same]) and torch.equal(lse[same], clean[1][same])
+
+
 def test_rows_without_any_weight():
     """All scores -infinity: no weight, as where nothing is seen."""
     pc = Paged([300, 70], 8, 2, 64, seed=42)
@@ -463,6 +499,30 @@ def test_evict_long_sequences(keep):
         t = torch.arange(nl, device=DEV)
         page, slot = pc.places(dst, s, nl, P)
         assert torch.equal(pc.cache.k_pool[page, slot], pc.k[s][4 * w[t // 4] + t % 4])
+
+
+def test_evict_past_the_tables():
+    """Blocks whose source lies behind the table's last column, or on a page that
+    is none, are flagged and not copied; the others are."""
+    pc = Paged([64, 40], 8, 2, 16, 64, seed=28, spare=8, width=4)
+    lens = torch.tensor([80, 40], dtype=torch.int32, device=DEV)  # 80 > 4 pages of 16
+    pc.cache.block_table[1, 1] = -7
+    dst = torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
+    dst[:, :3] = torch.arange(6, dtype=torch.int32, device=DEV).view(2, 3) + pc.first_spare
+    mass = torch.arange(20, dtype=torch.float32, device=DEV).flip(0).repeat(2, 1).contiguous()
+    b = qsa.alloc_evict(2, 20, 10)
+    qsa.qsa_evict(pc.dims, pc.cache, lens, mass, 10, 0, 4, dst, b.kept, b.new_lens, b.mass)
+    with pytest.raises(qsa.QsaError, match="flags=6"):
+        qsa.qsa_check_device_errors()
+    assert b.kept[0].tolist() == [0, 1, 2, 3, 4, 5, 16, 17, 18, 19]
+    assert b.kept[1].tolist() == list(range(10)) and b.new_lens.tolist() == [40, 40]
+    for s, tokens in ((0, range(24)), (1, [*range(16), *range(32, 40)])):
+        t = torch.tensor(list(tokens), device=DEV)
+        got = pc.cache.k_pool[dst[s].long()[t // 16], t % 16]
+        assert torch.equal(got, pc.k[s][t])
+    for s, tokens in ((0, range(24, 40)), (1, range(16, 32))):
+        t = torch.tensor(list(tokens), device=DEV)
+        assert bool(pc.cache.k_pool[dst[s].long()[t // 16], t % 16].isnan().all())
 
 
 def test_one_workspace_in_turn():
