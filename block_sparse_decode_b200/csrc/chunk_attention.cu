@@ -731,6 +731,9 @@ __global__ void __launch_bounds__(CA_THREADS, 1)
       ctl.pm[s][half][r] = l;
       both(true);
       l += ctl.pm[s][half ^ 1][r];
+      // (past 2^30 the maximum is rounded by 64 and more, and weights of 2^-127 and
+      // below or 2^128 and more would come of it)
+      if (m > -INFINITY && fabsf(m) > 0x1p30f) l = NAN;
       ok = wait_all(ofull + 8 * s, oph, abort_flag, p.err);
       oph ^= 1u;
       tc_fence_after();

@@ -434,7 +434,8 @@ size_t qsa_chunk_attention_workspace_size(const qsa_dims *dims, int32_t S, int32
  * of range raises flag 2 and leaves the values of its sequence's rows
  * undefined. The cache slots past L_s may hold anything; the K and V of
  * tokens below L_s must be finite. A row and head with a score (fp32) that is
- * NaN or +infinity gets NaN, its LSE too; one whose scores are all -infinity
+ * NaN or +infinity gets NaN, its LSE too, and so does one whose largest score is
+ * beyond +-7 * 10^8 (2^30 / log2 e); one whose scores are all -infinity gets
  * zeros and LSE -infinity. 0 <= S, Nq <= 65535. */
 qsa_status qsa_chunk_attention(const qsa_dims *dims, const qsa_cache *cache, int32_t S,
                                const int32_t *seq_lens, const int32_t *row_start, int32_t Nq,

@@ -459,6 +459,51 @@ def test_scores_that_are_not_finite_in_long_items():
     assert torch.equal(out[same], clean[0][same]) and torch.equal(lse[same], clean[1][same])
 
 
+@pytest.mark.parametrize("lens,chunks", [([3000, 200], [1, 1]), ([515, 70], [90, 70]), ([70001], [1])])
+def test_huge_scores(lens, chunks):
+    """Scores up to 2^29 give weights; a row whose largest is beyond 2^30 (in units of
+    log2) gets NaN and not, where the fp32 maximum was rounded up by 128 and more,
+    zeros. What is far below the largest score has no weight, however far."""
+    pc = Paged(lens, 8, 2, 64, seed=44)
+    pc.dims = dataclasses.replace(pc.dims, scale=0.125)
+    start, q = pc.rows(chunks, 21)
+    for s, (n, T) in enumerate(zip(lens, chunks)):
+        pc.k[s][:, :, :3] = 0
+        pc.k[s][(n - T) // 2, :, 0] = 1.0  # one token, seen by every row
+        pc.k[s][:, :, 1] = 1.0
+        page, slot = pc.places(pc.cache.block_table, s, n, 64)
+        pc.cache.k_pool[page, slot] = pc.k[s]
+    rows = [int(start[s]) + T - 1 - T // 3 for s, T in enumerate(chunks)]
+    q[rows] = 0
+    held = ((0, 0, 2.0 ** 32), (1, 0, -2.0 ** 36), (2, 1, 2.0 ** 32), (3, 1, -2.0 ** 32))
+    # (the first: the maximum is rounded up by 236; the second: down by 248)
+    past = [(4, 0, 1.984375 * 2.0 ** 34), (5, 0, 1.40625 * 2.0 ** 34), (6, 1, -1.984375 * 2.0 ** 36),
+            (7, 1, 1.8046875 * 2.0 ** 39)]
+    for h, i, v in (*held, *past):
+        q[rows, h, i] = v
+    b = attend(pc, start, q)
+    for h, _, _ in past:
+        assert bool(b.out[rows, h].isnan().all()) and bool(b.lse[rows, h].isnan().all())
+    ref, lse, size, _ = attention_ref(pc, chunks, q)
+    mine = torch.ones((q.shape[0], 8), dtype=torch.bool, device=DEV)
+    for h, _, _ in past:
+        mine[rows, h] = False
+    # Heads 2 and 3 have all scores equal, at 2^29: half a step of a part's LSE in
+    # fp32 is 2^29 / 2^24 = 32, so the parts' weights against each other may be off
+    # by e^32 either way, which leaves them any average of the values they see
+    for s, n in enumerate(pc.lens):
+        v = pc.v[s][:, :, None].float().expand(n, 2, 4, 128).reshape(n, 8, 128)[:, 2:4]
+        o = b.out[rows[s], 2:4]
+        slack = HALF * v.abs().amax(0)
+        assert bool((o <= v.amax(0) + slack).all()) and bool((o >= v.amin(0) - slack).all())
+    mine[rows, 2:4] = False
+    assert bool(((b.out.double() - ref).abs() <= (HALF + 2.0 ** -12) * size + 1e-6)[mine].all())
+    # (an LSE in fp32: half a step of it and of the maximum, once each more for log2)
+    mine[rows, 2:4] = True
+    err = (b.lse.double() - lse).abs()
+    assert bool((err <= 1e-3 + 2.0 ** -22 * lse.abs())[mine].all())
+
+
 def test_rows_without_any_weight():
     """All scores -infinity: no weight, as where nothing is seen."""
     pc = Paged([300, 70], 8, 2, 64, seed=42)
